@@ -1,0 +1,376 @@
+"""The measured cases of the rotary positions, the 8-bit activation checkpoints and
+the block-sparse attention step that trains on such checkpoints.
+
+`run` computes an operator in plain torch (fp32, angles and group scales in fp64) or,
+with `own` set, through the package's public calls:
+
+* ``rotary``: queries and keys [B, H, N, d] (views of the projections' [B, N, H, d], or
+  head-major) rotated by one position per token or by (t, h, w) grid positions, and for
+  training the gradients that come back through the rotation.
+* ``pack``: activations kept as 8-bit codes in groups of 32 with one exponent byte, and
+  read back; the values that the codes stand for are returned.
+* ``step``: attention under a given block mask whose q, k, v are kept in 8 bits for the
+  backward pass: o, and dq, dk, dv, the attention's gradients at the kept values.
+"""
+
+import math
+
+import torch
+
+own = False
+
+GROUP = 32
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+# ---------------------------------------------------------------- the cases
+def _rotary(name, B, N, Hq, Hk, d, rd, layout, order, dtype, train, grid="", start=0, factor=1.0):
+    return {"name": name, "op": "rotary", "B": B, "N": N, "Hq": Hq, "Hk": Hk, "d": d, "rd": rd, "layout": layout,
+            "order": order, "dtype": dtype, "train": train, "grid": grid, "start": start, "factor": factor}
+
+
+def _pack(name, rows, d, tensors, dtype):
+    return {"name": name, "op": "pack", "rows": rows, "d": d, "tensors": tensors, "dtype": dtype}
+
+
+def _step(name, B, H, N, d, bq, bkv, kept):
+    return {"name": name, "op": "step", "B": B, "H": H, "N": N, "d": d, "bq": bq, "bkv": bkv, "kept": kept}
+
+
+def listed():
+    return [
+        # one token of each of 8 sequences at a far position (context stretched 4x): the step of a decoder, latency alone
+        _rotary("rotary-token", 8, 1, 32, 8, 128, 128, "half", "bnhd", "bf16", False, start=131071, factor=4.0),
+        # the small test problem with a quarter of each head rotated, ragged length, fp32, gradients
+        _rotary("rotary-partial", 2, 1000, 2, 2, 64, 16, "half", "bhnd", "fp32", True, start=5),
+        # q and k of the 1.3B-shaped video layer, straight from the projections, with gradients
+        _rotary("rotary-1.3b", 1, 32760, 12, 12, 128, 128, "interleaved", "bnhd", "bf16", True, grid="21x30x52"),
+        # the 14B-shaped layer: the longest video the framework measures
+        _rotary("rotary-14b", 1, 75600, 40, 40, 128, 128, "interleaved", "bnhd", "bf16", True, grid="21x45x80"),
+        # q, k, v, o of the small test problem
+        _pack("pack-small", 1024, 64, 4, "bf16"),
+        # hidden states with a width that is no multiple of a group
+        _pack("pack-ragged", 32760, 1000, 1, "fp16"),
+        # q, k, v, o of the 1.3B-shaped layer
+        _pack("pack-1.3b", 393120, 128, 4, "bf16"),
+        # training steps: the small test problem, a ragged one with 64-row blocks, one of the sweep's lengths, and the
+        # 1.3B-shaped layer, the last two at 95% block sparsity
+        _step("step-small", 1, 2, 512, 64, 128, 64, 0.5),
+        _step("step-ragged", 2, 3, 1000, 64, 64, 128, 0.3),
+        _step("step-8k", 1, 12, 8192, 128, 128, 64, 0.05),
+        _step("step-1.3b", 1, 12, 32760, 128, 128, 64, 0.05),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))
+
+
+def draw(rng):
+    op = rng.choice(("rotary", "pack", "step"))
+    if op == "rotary":
+        d = rng.choice((64, 80, 96, 128, 256))
+        rd = rng.choice((d, d, d // 2, 16))
+        heads = _log(rng, 1, 40)
+        kv_heads = rng.choice((heads, heads, max(1, heads // 4)))
+        B = rng.choice((1, 1, 2, 3))
+        N = _log(rng, 1, max(2, min(75600, 75600 * 40 * 128 // (B * heads * d))))
+        grid = ""
+        if rng.random() < 0.4:
+            h, w = rng.randint(1, 64), rng.randint(1, 90)
+            grid = "%dx%dx%d" % (-(-N // (h * w)), h, w)
+        c = _rotary("", B, N, heads, kv_heads, d, rd, rng.choice(("interleaved", "half")), rng.choice(("bnhd", "bhnd")),
+                    rng.choice(("bf16", "bf16", "bf16", "fp16", "fp32")), rng.random() < 0.7, grid,
+                    0 if grid else rng.choice((0, 1000, 131071)), rng.choice((1.0, 4.0)))
+    elif op == "pack":
+        d = rng.choice((64, 80, 128, 200, 1000, 1536, 5120))
+        tensors = rng.randint(1, 4)
+        c = _pack("", _log(rng, 1, 393120 * 128 * 4 // (d * tensors)), d, tensors, rng.choice(("bf16", "bf16", "fp16", "fp32")))
+    else:
+        B, H = rng.choice((1, 1, 2)), rng.randint(1, 6)
+        bq, bkv = rng.choice(((128, 64), (128, 64), (128, 64), (64, 64), (64, 128), (256, 128)))
+        c = _step("", B, H, _log(rng, 64, 16000), rng.choice((64, 128)), bq, bkv, rng.choice((0.05, 0.1, 0.2)))
+    del c["name"]
+    return c
+
+
+# ---------------------------------------------------------------- the inputs
+def _generator(seed):
+    return torch.Generator(device="cuda").manual_seed(int(seed))
+
+
+def _pairs(case):
+    """Pairs of rotated elements per position axis."""
+    p = case["rd"] // 2
+    return (p - 2 * (p // 3), p // 3, p // 3) if case["grid"] else (p,)
+
+
+def _prepare_rotary(case, g):
+    B, N, d = case["B"], case["N"], case["d"]
+    dtype = DTYPES[case["dtype"]]
+
+    def heads(H, grad):
+        x = torch.randn((B, N, H, d) if case["order"] == "bnhd" else (B, H, N, d), generator=g, device="cuda").to(dtype)
+        x = x.transpose(1, 2) if case["order"] == "bnhd" else x
+        return x.requires_grad_(case["train"]) if grad else x
+
+    def gradient(H):  # as the attention hands it back: head-major
+        return torch.randn((B, H, N, d), generator=g, device="cuda").to(dtype)
+
+    # each axis has its own run of frequencies, as positions on a (t, h, w) grid take them
+    freqs = [10000.0 ** -(torch.arange(n, dtype=torch.float64) / n) for n in _pairs(case)]
+    if case["grid"]:
+        _, h, w = (int(x) for x in case["grid"].split("x"))
+        n = torch.arange(N, device="cuda")
+        positions = torch.stack((n // (h * w), n // w % h, n % w))
+    else:
+        begin = case["start"] + torch.randint(0, 1000, (B, 1), generator=g, device="cuda")
+        positions = begin + torch.arange(N, device="cuda")
+    f = case["factor"]
+    return {"q": heads(case["Hq"], True), "k": heads(case["Hk"], True),
+            "dq": gradient(case["Hq"]), "dk": gradient(case["Hk"]),
+            "inv_freq": torch.cat(freqs).cuda() / f, "positions": positions, "axes": _pairs(case),
+            "scale": 0.1 * math.log(f) + 1.0}
+
+
+def _prepare_pack(case, g):
+    def activations():
+        x = torch.randn(case["rows"], case["d"], generator=g, device="cuda")
+        x = x * torch.exp(torch.randn(case["rows"], 1, generator=g, device="cuda"))  # tokens differ in size
+        x[:, ::97] *= 20.0  # and a few channels stand out
+        return x.to(DTYPES[case["dtype"]])
+
+    return {"xs": [activations() for _ in range(case["tensors"])]}
+
+
+def _prepare_step(case, g):
+    B, H, N, d, bq, bkv = (case[x] for x in ("B", "H", "N", "d", "bq", "bkv"))
+    Tm, Tn = -(-N // bq), -(-N // bkv)
+    q, k, v, dout = (torch.randn(B, H, N, d, generator=g, device="cuda") for _ in range(4))
+    k = 0.5 * q + math.sqrt(0.75) * k  # a token attends to itself and its like
+    towards = q.mean(dim=2, keepdim=True)
+    sinks = 2 if N >= 64 else 0  # among a handful of keys they would take all the attention
+    k[:, :, :sinks] = 8.0 * math.sqrt(d) * towards / towards.norm(dim=-1, keepdim=True)
+    # the kept blocks: the first one, the ones on the diagonal and others at random; some rows keep more than others
+    mean = max(1.0, case["kept"] * Tn)
+    i = torch.arange(Tm, device="cuda")
+    many = (mean * (0.6 + 0.8 * ((i * 0.6180339887) % 1.0))).round().clamp(1, Tn).long()
+    score = torch.rand(B, H, Tm, Tn, generator=g, device="cuda")
+    score[:, :, i, (i * bq) // bkv] += 2.0
+    score[..., 0] += 1.0
+    kept = score.argsort(dim=-1, descending=True).argsort(dim=-1) < many[:, None]
+
+    def lists(keep):
+        n = keep.shape[-1]
+        ids = torch.where(keep, torch.arange(n, device="cuda"), n).sort(dim=-1).values
+        return keep.sum(-1).int(), ids.clamp(max=n - 1).int()
+
+    row_cnt, row_idx = lists(kept)
+    col_cnt, col_idx = lists(kept.transpose(-1, -2))
+    q, k, v = (x.to(torch.bfloat16).requires_grad_() for x in (q, k, v))
+    return {"q": q, "k": k, "v": v, "dout": dout.to(torch.bfloat16), "row_cnt": row_cnt, "row_idx": row_idx,
+            "col_cnt": col_cnt, "col_idx": col_idx, "width": int(row_cnt.max())}
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    make = {"rotary": _prepare_rotary, "pack": _prepare_pack, "step": _prepare_step}[case["op"]]
+    return {"case": case, **make(case, g)}
+
+
+# ---------------------------------------------------------------- the plain forms
+def _rotate(x, cos, sin, layout, rd):
+    """x [B, H, N, d] in fp32 rotated by cos, sin [B or 1, 1, N, rd / 2]."""
+    turn, rest = x[..., :rd], x[..., rd:]
+    if layout == "half":
+        a, b = turn[..., : rd // 2], turn[..., rd // 2:]
+        return torch.cat((a * cos - b * sin, a * sin + b * cos, rest), dim=-1)
+    a, b = turn[..., 0::2], turn[..., 1::2]
+    return torch.cat((torch.stack((a * cos - b * sin, a * sin + b * cos), dim=-1).flatten(-2), rest), dim=-1)
+
+
+def _angles(s):
+    """Position times frequency in fp64: [B or 1, 1, N, rd / 2]."""
+    pos = s["positions"].double()
+    if len(s["axes"]) == 1:
+        return pos[:, None, :, None] * s["inv_freq"]
+    per_pair = torch.repeat_interleave(pos, torch.tensor(s["axes"], device="cuda"), dim=0)
+    return (per_pair.t() * s["inv_freq"])[None, None]
+
+
+def _plain_rotary(s):
+    c = s["case"]
+    angle = _angles(s)
+    cos, sin = ((s["scale"] * f(angle)).float() for f in (torch.cos, torch.sin))
+    there = [_rotate(x.detach().float(), cos, sin, c["layout"], c["rd"]).to(x.dtype) for x in (s["q"], s["k"])]
+    if not c["train"]:
+        return there
+    return there + [_rotate(x.float(), cos, -sin, c["layout"], c["rd"]).to(x.dtype) for x in (s["dq"], s["dk"])]
+
+
+def _eight_bits(x):
+    """The values that x's 8-bit codes stand for, in fp64: per group of 32 of the last dimension the codes are
+    x * 2^(6 - e) to the nearest whole number, with e the exponent of the group's largest magnitude."""
+    d = x.shape[-1]
+    y = torch.nn.functional.pad(x.double(), (0, -d % GROUP)).unflatten(-1, (-1, GROUP))
+    most = y.abs().amax(dim=-1, keepdim=True)
+    e = (torch.frexp(most).exponent.long() - 7).clamp(min=-133)
+    step = (e + 1023 << 52).view(torch.float64)  # 2^e, whatever exp2 rounds to
+    codes = torch.round(y / step).clamp(-127, 127)
+    return (codes * step).flatten(-2)[..., :d]
+
+
+def _blocks(x, n, size):
+    """[B, H, N, d] -> [B * H, n, size, d] in fp32, zero rows behind the last."""
+    B, H, N, d = x.shape
+    return torch.nn.functional.pad(x.float(), (0, 0, 0, n * size - N)).view(B * H, n, size, d)
+
+
+def _plain_step(s):
+    c = s["case"]
+    B, H, N, d, bq, bkv = (c[x] for x in ("B", "H", "N", "d", "bq", "bkv"))
+    Tm, Tn, W = -(-N // bq), -(-N // bkv), s["width"]
+    scale = d ** -0.5
+    ids = s["row_idx"].view(B * H, Tm, Tn)[..., :W].long()
+    listed_ = torch.arange(W, device="cuda") < s["row_cnt"].view(B * H, Tm, 1)
+    column = ids[..., None] * bkv + torch.arange(bkv, device="cuda")
+    there = (listed_[..., None] & (column < N)).view(B * H, Tm, 1, W * bkv)
+    at = (ids + torch.arange(B * H, device="cuda")[:, None, None] * Tn).view(-1)
+
+    def gathered(x):  # the kept key blocks of each query block
+        return _blocks(x, Tn, bkv).view(B * H * Tn, bkv * d)[at].view(B * H, Tm, W * bkv, d)
+
+    def scattered(g):  # and what comes back to each key block
+        out = torch.zeros(B * H * Tn, bkv * d, device="cuda").index_add_(0, at, g.view(-1, bkv * d))
+        return out.view(B, H, Tn * bkv, d)[:, :, :N].to(torch.bfloat16)
+
+    def rows(x):
+        return x.reshape(B, H, Tm * bq, d)[:, :, :N].to(torch.bfloat16)
+
+    def attention(q, k, v):
+        logits = (_blocks(q, Tm, bq) @ gathered(k).transpose(-1, -2) * scale).masked_fill_(~there, -math.inf)
+        p = logits.sub_(logits.amax(-1, keepdim=True)).exp_()
+        p.div_(p.sum(-1, keepdim=True))
+        return p, p @ gathered(v)
+
+    q, k, v = (s[x].detach() for x in "qkv")
+    o = rows(attention(q, k, v)[1])
+    q, k, v = (_eight_bits(x).float() for x in (q, k, v))
+    p, kept_o = attention(q, k, v)
+    dout = _blocks(s["dout"], Tm, bq)
+    dv = scattered(p.transpose(-1, -2) @ dout)
+    ds = (dout @ gathered(v).transpose(-1, -2)).sub_((dout * kept_o).sum(-1, keepdim=True)).mul_(p)
+    del p
+    dq = rows(ds @ gathered(k) * scale)
+    dk = scattered(ds.transpose(-1, -2) @ _blocks(q, Tm, bq) * scale)
+    return [o, dq, dk, dv]
+
+
+# ---------------------------------------------------------------- one pass
+def run(state):
+    c = state["case"]
+    if c["op"] == "rotary":
+        if not own:
+            return _plain_rotary(state)
+        from trainable_block_sparse_pooled_b200.rotary import apply_rotary
+        q, k = apply_rotary(state["q"], state["k"], inv_freq=state["inv_freq"], positions=state["positions"],
+                            layout=c["layout"], axes=state["axes"], scale=state["scale"])
+        if not c["train"]:
+            return [q, k]
+        return [q, k, *torch.autograd.grad((q, k), (state["q"], state["k"]), (state["dq"], state["dk"]))]
+    if c["op"] == "pack":
+        if not own:
+            return [_eight_bits(x).to(x.dtype) for x in state["xs"]]
+        from trainable_block_sparse_pooled_b200.checkpoint import pack8, unpack8
+        return list(unpack8(*pack8(*state["xs"])))
+    if not own:
+        return _plain_step(state)
+    from trainable_block_sparse_pooled_b200.autograd import sparse_attention
+    from trainable_block_sparse_pooled_b200.binding import Mask
+    mask = Mask(state["row_cnt"], state["row_idx"], state["col_cnt"], state["col_idx"])
+    leaves = (state["q"], state["k"], state["v"])
+    o = sparse_attention(*leaves, mask=mask, bq=c["bq"], bkv=c["bkv"], checkpoint="int8")
+    return [o, *torch.autograd.grad(o, leaves, state["dout"])]
+
+
+def work(case):
+    """Each input read once, each output written once; the checkpoints written and read once."""
+    if case["op"] == "rotary":
+        n = case["B"] * case["N"] * (case["Hq"] + case["Hk"]) * case["d"] * (2 if case["train"] else 1)
+        return {"bytes": 2 * n * DTYPES[case["dtype"]].itemsize, "flops": 3 * n}
+    if case["op"] == "pack":
+        n, groups = case["rows"] * case["d"], case["rows"] * -(-case["d"] // GROUP)
+        return {"bytes": 2 * case["tensors"] * (n * (DTYPES[case["dtype"]].itemsize + 1) + groups), "flops": 0}
+    n = case["B"] * case["H"] * case["N"] * case["d"]
+    pairs = n / case["d"] * max(case["bkv"], case["kept"] * case["N"])
+    return {"bytes": 16 * n + 2 * 3 * (n + n // GROUP), "flops": 14 * case["d"] * min(pairs, n / case["d"] * case["N"])}
+
+
+# ---------------------------------------------------------------- in 64 bits
+def _exact_rotary(case, s):
+    def turned(x, sign):
+        x = x.detach().double()
+        z = torch.polar(torch.full_like(angle, s["scale"]), sign * angle)
+        half, rd = case["rd"] // 2, case["rd"]
+        first = torch.arange(half, device="cuda") * (1 if case["layout"] == "half" else 2)
+        second = first + (half if case["layout"] == "half" else 1)
+        w = torch.complex(x[..., first], x[..., second]) * z
+        y = x.clone()
+        y[..., first], y[..., second] = w.real, w.imag
+        return y
+
+    pos = s["positions"].double().reshape(1, len(case["grid"].split("x")), -1) if case["grid"] \
+        else s["positions"].double().unsqueeze(1)
+    axis = [a for a, n in enumerate(s["axes"]) for _ in range(n)]
+    angle = (pos[:, axis, :] * s["inv_freq"][:, None]).transpose(1, 2).unsqueeze(1)
+    return [turned(s["q"], 1), turned(s["k"], 1)] + ([turned(s["dq"], -1), turned(s["dk"], -1)] if case["train"] else [])
+
+
+def _exact_values(x):
+    """The kept values from the bits of the largest magnitude's exponent."""
+    d = x.shape[-1]
+    y = torch.zeros(*x.shape[:-1], -(-d // GROUP) * GROUP, dtype=torch.float64, device="cuda")
+    y[..., :d] = x
+    y = y.view(*x.shape[:-1], -1, GROUP)
+    bits = y.abs().max(dim=-1, keepdim=True).values.view(torch.int64)
+    unit = ((bits >> 52 << 52).view(torch.float64) / 64.0).clamp(min=2.0 ** -133)
+    below = torch.floor(y / unit)
+    left = y / unit - below
+    code = below + ((left > 0.5) | ((left == 0.5) & (torch.remainder(below, 2.0) == 1.0))).double()
+    return (torch.minimum(torch.maximum(code, code.new_tensor(-127.0)), code.new_tensor(127.0)) * unit).reshape(*x.shape[:-1], -1)[..., :d]
+
+
+def _exact_step(case, s):
+    """Dense attention under the token mask that the lists mean, some query rows of one head at a time."""
+    B, H, N, d, bq, bkv = (case[x] for x in ("B", "H", "N", "d", "bq", "bkv"))
+    Tm, Tn = s["row_idx"].shape[-2:]
+    outs = [torch.zeros(B, H, N, d, dtype=torch.float64, device="cuda") for _ in range(4)]
+    many = max(bq, (1 << 27) // N // bq * bq)
+    for b in range(B):
+        for h in range(H):
+            q, k, v, dout = (s[x][b, h].detach().double() for x in ("q", "k", "v", "dout"))
+            q8, k8, v8 = (_exact_values(s[x][b, h].detach()) for x in ("q", "k", "v"))
+            keep = torch.zeros(Tm, Tn + 1, dtype=torch.bool, device="cuda")
+            slot = torch.arange(Tn, device="cuda") < s["row_cnt"][b, h, :, None]
+            keep.scatter_(1, torch.where(slot, s["row_idx"][b, h].long(), Tn), True)
+            for r in range(0, N, many):
+                i = torch.arange(r, min(N, r + many), device="cuda")
+                off = ~keep[:, :Tn][i // bq][:, torch.arange(N, device="cuda") // bkv]
+                a = torch.softmax((q[i] @ k.t() / math.sqrt(d)).masked_fill_(off, -math.inf), dim=1)
+                outs[0][b, h, i] = a @ v
+                a = torch.softmax((q8[i] @ k8.t() / math.sqrt(d)).masked_fill_(off, -math.inf), dim=1)
+                outs[3][b, h] += a.t() @ dout[i]
+                delta = (dout[i] * (a @ v8)).sum(1, keepdim=True)
+                a *= dout[i] @ v8.t() - delta
+                outs[1][b, h, i] = a @ k8 / math.sqrt(d)
+                outs[2][b, h] += a.t() @ q8[i] / math.sqrt(d)
+    return outs
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "rotary":
+        return _exact_rotary(case, s)
+    if case["op"] == "pack":
+        return [_exact_values(x) for x in s["xs"]]
+    return _exact_step(case, s)
