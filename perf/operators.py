@@ -163,7 +163,7 @@ def _prepare_step(case, g):
     def lists(keep):
         n = keep.shape[-1]
         ids = torch.where(keep, torch.arange(n, device="cuda"), n).sort(dim=-1).values
-        return keep.sum(-1).int(), ids.clamp(max=n - 1).int()
+        return keep.sum(-1).int().contiguous(), ids.clamp(max=n - 1).int().contiguous()
 
     row_cnt, row_idx = lists(kept)
     col_cnt, col_idx = lists(kept.transpose(-1, -2))
