@@ -93,10 +93,11 @@ typedef struct {
   uint8_t* bitmap;
 } spa2_mask;
 
-enum { SPA2_OP_MASK = 0, SPA2_OP_FWD = 1, SPA2_OP_BWD = 2, SPA2_OP_SELECT = 3 };
+enum { SPA2_OP_MASK = 0, SPA2_OP_FWD = 1, SPA2_OP_BWD = 2, SPA2_OP_SELECT = 3, SPA2_OP_BWD_CKPT = 4 };
 
-/* Element type of the gradient outputs of spa2_sparse_attn_bwd. */
-enum { SPA2_DTYPE_BF16 = 0, SPA2_DTYPE_F32 = 1 };
+/* Element types: the gradient outputs of the backward calls are BF16 or F32, the
+ * tensors of spa2_rotary, spa2_pack8 and spa2_unpack8 any of the three. */
+enum { SPA2_DTYPE_BF16 = 0, SPA2_DTYPE_F32 = 1, SPA2_DTYPE_F16 = 2 };
 
 /* ABI version of this header (bumped on any incompatible change). */
 #define SPA2_ABI_VERSION 1
@@ -239,6 +240,117 @@ SPA2_API spa2_status spa2_sparse_attn_bwd(const void* q, const void* k, const vo
                                           int d, int bq, int bkv, const spa2_mask* mask, float softmax_scale,
                                           void* dq, void* dk, void* dv, int grad_dtype, void* ws, size_t ws_bytes,
                                           spa2_stream_t stream);
+
+/*
+ * Rotary positions: queries and keys turned by their tokens' positions before
+ * they enter the mask and the attention, and gradients turned back. With rd =
+ * rotary_dim, pair p (0 <= p < rd / 2) of a head's row is its elements (2p,
+ * 2p + 1) (SPA2_ROTARY_INTERLEAVED) or (p, p + rd / 2) (SPA2_ROTARY_HALF);
+ *   theta = position(axis of p, token) * inv_freq[p],
+ *   (a, b) -> scale * (a cos theta - b sin theta, a sin theta + b cos theta),
+ * and elements rd .. d - 1 are copied as they are. `inverse` turns by -theta,
+ * the transpose of the forward map, which is its backward pass.
+ * Angles are reduced in fp64 (good to fp32 accuracy while |theta| < 2^31), the
+ * rotation runs in fp32 and is rounded once to the element type.
+ *   t, n      : 1 or 2 tensors (queries and keys) of the same B, N, d and type
+ *               turned by one launch; heads may differ. Strides are in elements
+ *               (batch, head, token); the d elements of a row are contiguous.
+ *               x and y must not overlap.
+ *   positions : device int32 or int64 (position_bytes 4 or 8) with the given
+ *               strides in elements, or NULL for 0 .. N-1 (one axis only)
+ *   axes      : 1 .. SPA2_ROTARY_MAX_AXES position axes; axis a turns the next
+ *               pairs[a] pairs, sum of pairs = rd / 2. Video tokens take three:
+ *               time, height and width.
+ *   inv_freq  : device fp64 [rd / 2], radians per position
+ * Supported set: 1 <= d <= 1024, rd even with 2 <= rd <= d, B, N, heads >= 1,
+ * B * N <= 2^31 - 1, heads of all tensors together <= 65535. No workspace; the
+ * call needs none of the status words (it has no device-side failure).
+ */
+enum { SPA2_ROTARY_INTERLEAVED = 0, SPA2_ROTARY_HALF = 1 };
+#define SPA2_ROTARY_MAX_AXES 4
+typedef struct {
+  const void* x;
+  void* y;
+  int heads;
+  int64_t x_stride[3]; /* batch, head, token */
+  int64_t y_stride[3];
+} spa2_rotary_tensor;
+typedef struct {
+  const void* positions;
+  int position_bytes;
+  int64_t position_stride[3]; /* batch, axis, token */
+  int axes;
+  int pairs[SPA2_ROTARY_MAX_AXES];
+  const double* inv_freq;
+  int rotary_dim;
+  int layout; /* SPA2_ROTARY_* */
+  float scale;
+} spa2_rotary_spec;
+SPA2_API spa2_status spa2_rotary(const spa2_rotary_tensor* t, int n, int B, int N, int d, int dtype,
+                                 const spa2_rotary_spec* spec, int inverse, spa2_stream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits. Every group of 32 consecutive elements of a
+ * row (the last group of a row may be shorter) is kept as one exponent byte E and
+ * one int8 code per element:
+ *   E     = biased fp32 exponent field of the group's largest magnitude (0 when
+ *           that is zero or an fp32 subnormal),
+ *   code  = x * 2^(133 - E) rounded to the nearest integer, ties to even, clamped
+ *           to [-127, 127],
+ *   value = code * 2^(E - 133).
+ * The step 2^(E - 133) is 1/64 to 1/128 of the largest magnitude, so a value is
+ * off by at most half a step (by less than one where the clamp acts). Codes have 7
+ * significant bits and the step is a power of two, so every value is exact in
+ * bf16, fp16 and fp32: reading a checkpoint back rounds nothing. E = 255 marks a
+ * group that held an infinity or a NaN; all its values read back as NaN.
+ *   spa2_pack8   reads x [rows, d], writes codes [rows, d] and exps
+ *                [rows, ceil(d / 32)]
+ *   spa2_unpack8 reads codes and exps, writes the values to x
+ *   t, n : 1 .. SPA2_PACK8_MAX tensors of one element type, done by one launch;
+ *          contiguous, x aligned to its element, codes and exps to 1 byte, no
+ *          two of them overlapping. rows * d <= 2^40; rows = 0 is allowed.
+ * No workspace and no device-side failure.
+ */
+#define SPA2_PACK8_GROUP 32
+#define SPA2_PACK8_MAX 8
+typedef struct {
+  void* x;
+  int8_t* codes;
+  uint8_t* exps;
+  int64_t rows;
+  int64_t d;
+} spa2_pack8_tensor;
+SPA2_API spa2_status spa2_pack8(const spa2_pack8_tensor* t, int n, int dtype, spa2_stream_t stream);
+SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, spa2_stream_t stream);
+
+/*
+ * The sparse attention step on 8-bit checkpoints. spa2_sparse_attn_fwd_ckpt is
+ * spa2_sparse_attn_fwd (same o, bit for bit) and also writes q, k, v as 8-bit
+ * checkpoints; nothing else needs to be kept for the backward pass (3.1 bytes per
+ * element of q instead of the 10 of q, k, v, o and o_lo in bf16).
+ * spa2_sparse_attn_bwd_ckpt reads the checkpoints, computes the attention again
+ * from their values (LSE and D = rowsum(dO * O) in the workspace, O itself is not
+ * stored) and writes dQ, dK, dV: the gradients of the attention at the kept
+ * values, with the arithmetic of spa2_sparse_attn_bwd.
+ * Keeping O and LSE instead of recomputing them is cheaper but not close: with q,
+ * k, v rounded to 8 bits and O, LSE not, the rows of dS no longer sum to zero,
+ * and sink keys of 8x norm amplify that to 12% of dQ (4% with recomputation).
+ *   q8, k8, v8 : codes and exps of [B*H*N, d] rows (x, rows and d are ignored);
+ *                codes 16-byte aligned, exps 4-byte aligned
+ *   lse        : [B, H, N] fp32, or NULL when it is not wanted
+ *   ws         : spa2_workspace_bytes(SPA2_OP_FWD, ...) for the forward and
+ *                spa2_workspace_bytes(SPA2_OP_BWD_CKPT, ...) for the backward
+ */
+SPA2_API spa2_status spa2_sparse_attn_fwd_ckpt(const void* q, const void* k, const void* v, int B, int H, int N,
+                                               int d, int bq, int bkv, const spa2_mask* mask, float softmax_scale,
+                                               void* o, float* lse, const spa2_pack8_tensor* q8,
+                                               const spa2_pack8_tensor* k8, const spa2_pack8_tensor* v8, void* ws,
+                                               size_t ws_bytes, spa2_stream_t stream);
+SPA2_API spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pack8_tensor* k8,
+                                               const spa2_pack8_tensor* v8, const void* dout, int B, int H, int N,
+                                               int d, int bq, int bkv, const spa2_mask* mask, float softmax_scale,
+                                               void* dq, void* dk, void* dv, int grad_dtype, void* ws,
+                                               size_t ws_bytes, spa2_stream_t stream);
 
 /*
  * Synchronises `stream`, then reads and clears the status word at the start

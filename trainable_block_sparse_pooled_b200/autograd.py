@@ -20,7 +20,14 @@ once such a copy has landed with an error in it, and `check_errors()` waits for
 every pending copy and raises.
 
 Workspaces are cached per (shape, device, CUDA stream): calls on different
-streams never share scratch memory.
+streams never share scratch memory. A call that is captured into a CUDA graph gets
+workspaces of its own, from the graph's memory, and its device-side errors are not
+reported (a replay reads no status word).
+
+`sparse_attention(..., checkpoint="int8")` keeps q, k and v for the backward pass as
+8-bit checkpoints (module `checkpoint`) and nothing else of their size; the
+backward pass computes the attention again from the kept values and returns its
+gradients there. `rotary=` turns q and k by their positions first (module `rotary`).
 """
 
 from __future__ import annotations
@@ -30,6 +37,8 @@ from collections import deque
 import torch
 
 from . import binding as b
+from .checkpoint import Packed
+from .rotary import Rotary, apply_rotary
 
 _cache: dict = {}
 
@@ -78,7 +87,23 @@ class _StatusWatch:
                 raise b.Spa2Error(code, f"device status of sparse_attention (op {op})")
 
 
+class _NoWatch:
+    """In the place of a _StatusWatch while a CUDA graph is captured: neither event
+    queries nor copies that a replay would repeat into a stale slot."""
+
+    def after(self, ops):
+        pass
+
+    def poll(self):
+        pass
+
+
 def _spa(B, H, N, d, device, bq=b.BQ, bkv=b.BKV) -> b.Spa2:
+    if torch.cuda.is_current_stream_capturing():
+        # graphs replay on any stream, two of them at once: each call owns its workspaces
+        s = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv)
+        s.watch = _NoWatch()
+        return s
     stream = torch.cuda.current_stream(device).cuda_stream
     key = (B, H, N, d, bq, bkv, str(device), stream)
     s = _cache.get(key)
@@ -131,11 +156,65 @@ class SparseAttentionFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do, _row_cnt_grad):
         q, k, v, o, lse, o_lo = ctx.saved_tensors
-        ctx.spa.watch.poll()
-        dq, dk, dv = ctx.spa.bwd(q, k, v, o, lse, do.contiguous(), ctx.mask, ctx.scale, o_lo=o_lo,
-                                 grad_dtype=b.DTYPE_BF16)
-        ctx.spa.watch.after([b.OP_BWD])
+        spa = ctx.spa
+        if torch.cuda.is_current_stream_capturing():
+            spa = _spa(spa.B, spa.H, spa.N, spa.d, spa.device, spa.bq, spa.bkv)
+        spa.watch.poll()
+        dq, dk, dv = spa.bwd(q, k, v, o, lse, do.contiguous(), ctx.mask, ctx.scale, o_lo=o_lo,
+                             grad_dtype=b.DTYPE_BF16)
+        spa.watch.after([b.OP_BWD])
         return dq, dk, dv, None, None, None, None, None, None
+
+
+class CheckpointedAttentionFunction(torch.autograd.Function):
+    """SparseAttentionFunction with q, k, v kept in 8 bits for the backward pass: the
+    same o, and the gradients of the attention at the kept values."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, k_frac: float, p_frac: float, scale: float, mask: b.Mask | None, bq: int, bkv: int):
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        B, H, N, d = q.shape
+        s = _spa(B, H, N, d, q.device, bq, bkv)
+        ops = [b.OP_FWD]
+        if mask is None:
+            mask = s.block_mask(q, k, k_frac, p_frac)
+            ops.insert(0, b.OP_MASK)
+        o, kept = s.fwd_ckpt(q, k, v, mask, scale)
+        s.watch.after(ops)
+        ctx.save_for_backward(*(p.data for p in kept))
+        ctx.mask, ctx.scale, ctx.blocks = mask, scale, (bq, bkv)
+        row_cnt = mask.row_cnt.clone()  # the kept-block counts (a copy: a reused mask serves many calls)
+        ctx.mark_non_differentiable(row_cnt)
+        return o, row_cnt
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, _row_cnt_grad):
+        B, H, N, d = do.shape
+        s = _spa(B, H, N, d, do.device, *ctx.blocks)
+        kept = tuple(Packed(data, do.shape, do.dtype) for data in ctx.saved_tensors)
+        dq, dk, dv = s.bwd_ckpt(kept, do.contiguous(), ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
+        s.watch.after([b.OP_BWD_CKPT])
+        return dq, dk, dv, None, None, None, None, None, None
+
+
+def _check_attention(q, k, v, mask, bq, bkv):
+    """What the checkpointed call checks before it touches the device."""
+    if any(x.dtype != torch.bfloat16 for x in (q, k, v)):
+        raise TypeError("sparse_attention expects bf16 q, k, v")
+    if q.dim() != 4 or k.shape != q.shape or v.shape != q.shape:
+        raise ValueError("sparse_attention expects q, k, v of one shape [B, H, N, d]")
+    if any(x.device != q.device or x.device.type != "cuda" for x in (q, k, v)):
+        raise ValueError("sparse_attention expects q, k, v on one CUDA device")
+    if mask is not None:
+        B, H, N, _ = q.shape
+        Tm, Tn = b.block_counts(N, bq, bkv)
+        want = {"row_cnt": (B, H, Tm), "row_idx": (B, H, Tm, Tn), "col_cnt": (B, H, Tn), "col_idx": (B, H, Tn, Tm)}
+        for name, shape in want.items():
+            t = getattr(mask, name)
+            if t is None or tuple(t.shape) != shape or t.device != q.device or t.dtype != torch.int32 \
+                    or not t.is_contiguous():
+                raise ValueError("mask does not belong to a problem of this shape and device")
 
 
 def block_mask(q, k, k_frac: float, p_frac: float, bq: int = b.BQ, bkv: int = b.BKV) -> b.Mask:
@@ -152,12 +231,31 @@ def block_mask(q, k, k_frac: float, p_frac: float, bq: int = b.BQ, bkv: int = b.
 
 
 def sparse_attention(q, k, v, k_frac: float = 0.0, p_frac: float = 0.0, scale: float = 0.0,
-                     return_mask: bool = False, mask: b.Mask | None = None, bq: int = b.BQ, bkv: int = b.BKV):
+                     return_mask: bool = False, mask: b.Mask | None = None, bq: int = b.BQ, bkv: int = b.BKV,
+                     checkpoint: str | None = None, rotary: Rotary | None = None):
     """Differentiable hybrid block-sparse attention with query blocks of bq rows
     (64, 128 or 256) and key/value blocks of bkv rows (64 or 128).
 
     With `mask` (from `block_mask` on a problem of the same shape and block
     sizes) the given mask is used as is and k_frac, p_frac are ignored.
+
+    checkpoint="int8" keeps q, k, v in 8 bits for the backward pass (3.1 bytes per
+    element of q in place of 10) and computes the attention again there: the same o,
+    and its gradients at the kept values. Where no gradient is wanted nothing is kept.
+
+    `rotary` turns q and k before the mask and the attention; the mask given by
+    `mask` is one of turned q and k.
     """
-    o, row_cnt = SparseAttentionFunction.apply(q, k, v, k_frac, p_frac, scale, mask, bq, bkv)
+    if checkpoint not in (None, "int8"):
+        raise ValueError(f"unknown checkpoint {checkpoint!r}: None or 'int8'")
+    if rotary is not None:
+        q, k = apply_rotary(q, k, inv_freq=rotary.inv_freq, positions=rotary.positions, layout=rotary.layout,
+                            axes=rotary.axes, scale=rotary.scale)
+    function = SparseAttentionFunction
+    if checkpoint is not None:
+        _check_attention(q, k, v, mask, bq, bkv)
+        if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+            function = CheckpointedAttentionFunction
+    with b.on_device(q.device):
+        o, row_cnt = function.apply(q, k, v, k_frac, p_frac, scale, mask, bq, bkv)
     return (o, row_cnt) if return_mask else o

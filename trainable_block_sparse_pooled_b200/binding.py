@@ -10,6 +10,7 @@ fails, an exception is raised.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -22,8 +23,11 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "spa2.h")
 
 (OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_WORKSPACE, ERR_DEVICE_BOUNDS,
  ERR_RANGE) = range(8)
-OP_MASK, OP_FWD, OP_BWD, OP_SELECT = range(4)
-DTYPE_BF16, DTYPE_F32 = 0, 1
+OP_MASK, OP_FWD, OP_BWD, OP_SELECT, OP_BWD_CKPT = range(5)
+DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
+ROTARY_INTERLEAVED, ROTARY_HALF = 0, 1
+ROTARY_MAX_AXES = 4
+PACK8_GROUP, PACK8_MAX = 32, 8
 BQ, BKV = 128, 64
 
 
@@ -41,6 +45,40 @@ class spa2_mask(ctypes.Structure):
         ("col_idx", ctypes.c_void_p),
         ("pbar", ctypes.c_void_p),
         ("bitmap", ctypes.c_void_p),
+    ]
+
+
+class spa2_rotary_tensor(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("heads", ctypes.c_int),
+        ("x_stride", ctypes.c_int64 * 3),
+        ("y_stride", ctypes.c_int64 * 3),
+    ]
+
+
+class spa2_rotary_spec(ctypes.Structure):
+    _fields_ = [
+        ("positions", ctypes.c_void_p),
+        ("position_bytes", ctypes.c_int),
+        ("position_stride", ctypes.c_int64 * 3),
+        ("axes", ctypes.c_int),
+        ("pairs", ctypes.c_int * ROTARY_MAX_AXES),
+        ("inv_freq", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int),
+        ("layout", ctypes.c_int),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class spa2_pack8_tensor(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("codes", ctypes.c_void_p),
+        ("exps", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("d", ctypes.c_int64),
     ]
 
 
@@ -65,6 +103,18 @@ _SIGS = {
     "spa2_sparse_attn_bwd": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 6
                              + [ctypes.POINTER(spa2_mask), ctypes.c_float] + [ctypes.c_void_p] * 3
                              + [ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "spa2_rotary": (ctypes.c_int, [ctypes.POINTER(spa2_rotary_tensor)] + [ctypes.c_int] * 5
+                    + [ctypes.POINTER(spa2_rotary_spec), ctypes.c_int, ctypes.c_void_p]),
+    "spa2_pack8": (ctypes.c_int, [ctypes.POINTER(spa2_pack8_tensor), ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "spa2_unpack8": (ctypes.c_int, [ctypes.POINTER(spa2_pack8_tensor), ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "spa2_sparse_attn_fwd_ckpt": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int] * 6
+                                  + [ctypes.POINTER(spa2_mask), ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]
+                                  + [ctypes.POINTER(spa2_pack8_tensor)] * 3
+                                  + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "spa2_sparse_attn_bwd_ckpt": (ctypes.c_int, [ctypes.POINTER(spa2_pack8_tensor)] * 3 + [ctypes.c_void_p]
+                                  + [ctypes.c_int] * 6 + [ctypes.POINTER(spa2_mask), ctypes.c_float]
+                                  + [ctypes.c_void_p] * 3 + [ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
+                                                             ctypes.c_void_p]),
     "spa2_stream_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "spa2_debug_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_longlong]),
     "spa2_debug_timeout_probe": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
@@ -142,6 +192,33 @@ def spa2_sparse_attn_bwd(q, k, v, o, o_lo, lse, dout, B, H, N, d, bq, bkv, mask:
                                       dq, dk, dv, grad_dtype, ws, ws_bytes, stream)
 
 
+def spa2_rotary(tensors, B, N, d, dtype, spec: spa2_rotary_spec, inverse, stream) -> int:
+    """`tensors`: a ctypes array of spa2_rotary_tensor."""
+    return lib().spa2_rotary(tensors, len(tensors), B, N, d, dtype, ctypes.byref(spec), 1 if inverse else 0, stream)
+
+
+def spa2_pack8(tensors, dtype, stream) -> int:
+    """`tensors`: a ctypes array of spa2_pack8_tensor."""
+    return lib().spa2_pack8(tensors, len(tensors), dtype, stream)
+
+
+def spa2_unpack8(tensors, dtype, stream) -> int:
+    return lib().spa2_unpack8(tensors, len(tensors), dtype, stream)
+
+
+def spa2_sparse_attn_fwd_ckpt(q, k, v, B, H, N, d, bq, bkv, mask: spa2_mask, scale, o, lse, q8: spa2_pack8_tensor,
+                              k8: spa2_pack8_tensor, v8: spa2_pack8_tensor, ws, ws_bytes, stream) -> int:
+    return lib().spa2_sparse_attn_fwd_ckpt(q, k, v, B, H, N, d, bq, bkv, ctypes.byref(mask), scale, o, lse,
+                                           ctypes.byref(q8), ctypes.byref(k8), ctypes.byref(v8), ws, ws_bytes, stream)
+
+
+def spa2_sparse_attn_bwd_ckpt(q8: spa2_pack8_tensor, k8: spa2_pack8_tensor, v8: spa2_pack8_tensor, dout, B, H, N, d,
+                              bq, bkv, mask: spa2_mask, scale, dq, dk, dv, grad_dtype, ws, ws_bytes, stream) -> int:
+    return lib().spa2_sparse_attn_bwd_ckpt(ctypes.byref(q8), ctypes.byref(k8), ctypes.byref(v8), dout, B, H, N, d, bq,
+                                           bkv, ctypes.byref(mask), scale, dq, dk, dv, grad_dtype, ws, ws_bytes,
+                                           stream)
+
+
 def spa2_stream_status(ws, stream) -> int:
     return lib().spa2_stream_status(ws, stream)
 
@@ -202,6 +279,14 @@ def block_counts(N: int, bq: int = BQ, bkv: int = BKV) -> tuple[int, int]:
 
 def _stream(torch):
     return torch.cuda.current_stream().cuda_stream
+
+
+def on_device(device):
+    """A context in which `device` is the current CUDA device (a launch goes to the current device's stream)."""
+    import torch
+    if device.type != "cuda" or device.index in (None, torch.cuda.current_device()):
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 class Spa2:
@@ -275,6 +360,41 @@ class Spa2:
                                     self.B, self.H, self.N, self.d, self.bq, self.bkv, cm, float(scale), dq.data_ptr(),
                                     dk.data_ptr(), dv.data_ptr(), int(grad_dtype), ws.data_ptr(), ws.numel(),
                                     _stream(t)), "spa2_sparse_attn_bwd")
+        return dq, dk, dv
+
+    def _ckpt_ws(self):
+        """The workspace of bwd_ckpt, allocated at its first call (it holds the kept values in bf16)."""
+        ws = self.ws.get(OP_BWD_CKPT)
+        if ws is None:
+            n = lib().spa2_workspace_bytes(OP_BWD_CKPT, self.B, self.H, self.N, self.d, self.bq, self.bkv)
+            ws = self.ws[OP_BWD_CKPT] = self.torch.zeros(n, dtype=self.torch.uint8, device=self.device)
+        return ws
+
+    def fwd_ckpt(self, q, k, v, mask: Mask, scale=0.0, lse=None):
+        """O (bf16) and the 8-bit checkpoints of q, k, v (checkpoint.Packed), all that bwd_ckpt needs."""
+        from .checkpoint import Packed
+        t = self.torch
+        o = t.empty_like(q)
+        kept = tuple(Packed.empty_like(x) for x in (q, k, v))
+        cm = mask.c()
+        ws = self.ws[OP_FWD]
+        _check(spa2_sparse_attn_fwd_ckpt(q.data_ptr(), k.data_ptr(), v.data_ptr(), self.B, self.H, self.N, self.d,
+                                         self.bq, self.bkv, cm, float(scale), o.data_ptr(),
+                                         None if lse is None else lse.data_ptr(), *(p.c() for p in kept),
+                                         ws.data_ptr(), ws.numel(), _stream(t)), "spa2_sparse_attn_fwd_ckpt")
+        return o, kept
+
+    def bwd_ckpt(self, kept, dout, mask: Mask, scale=0.0, grad_dtype=DTYPE_F32):
+        """dQ, dK, dV at the values of the checkpoints `kept` (from fwd_ckpt or checkpoint.pack8)."""
+        t = self.torch
+        gt = t.float32 if grad_dtype == DTYPE_F32 else t.bfloat16
+        dq, dk, dv = (t.empty(self.B, self.H, self.N, self.d, dtype=gt, device=dout.device) for _ in range(3))
+        cm = mask.c()
+        ws = self._ckpt_ws()
+        _check(spa2_sparse_attn_bwd_ckpt(*(p.c() for p in kept), dout.data_ptr(), self.B, self.H, self.N, self.d,
+                                         self.bq, self.bkv, cm, float(scale), dq.data_ptr(), dk.data_ptr(),
+                                         dv.data_ptr(), int(grad_dtype), ws.data_ptr(), ws.numel(), _stream(t)),
+               "spa2_sparse_attn_bwd_ckpt")
         return dq, dk, dv
 
     def check(self, op=None):

@@ -147,6 +147,31 @@ static BwdWs bwd_ws(void* ws, const Shape& s) {
   return w;
 }
 
+// the backward on 8-bit checkpoints: the backward's own workspace, then the kept
+// values of q, k, v and what the recomputed forward leaves
+struct CkptWs {
+  BwdWs b;
+  float* lse;
+  void *q, *k, *v;  // [BH, N, d] bf16
+  void* v16;        // fp16 copy of v
+  void *o, *o_lo;
+  size_t bytes;
+};
+static CkptWs ckpt_ws(void* ws, const Shape& s) {
+  CkptWs w{};
+  w.b = bwd_ws(ws, s);
+  char* base = static_cast<char*>(ws);
+  size_t off = w.b.bytes;
+  w.lse = reinterpret_cast<float*>(base + off);
+  off += al256((size_t)s.BH * s.N * 4);
+  for (void** p : {&w.q, &w.k, &w.v, &w.v16, &w.o, &w.o_lo}) {
+    *p = base + off;
+    off += al256((size_t)s.BH * s.N * s.d * 2);
+  }
+  w.bytes = off;
+  return w;
+}
+
 // TMA descriptors ------------------------------------------------------------
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -228,6 +253,11 @@ static bool make_map_f32(CUtensorMap* m, const void* ptr, const Shape& s, int ro
   return get_map(m, ptr, s, rows, MAP_F32);
 }
 
+// the codes and exponents of an 8-bit checkpoint, as the attention calls take them
+static bool packed_ok(const spa2_pack8_tensor* t) {
+  return t && t->codes && t->exps && aligned(t->codes, 16) && aligned(t->exps, 4);
+}
+
 static int topk_count(float k_frac, int Tn) {
   long long K = (long long)floor((double)k_frac * (double)Tn + 0.5);
   if (K < 1) K = 1;
@@ -300,6 +330,7 @@ size_t spa2_workspace_bytes(int op, int B, int H, int N, int d, int bq, int bkv)
     case SPA2_OP_MASK: return mask_ws(nullptr, s).bytes;
     case SPA2_OP_FWD: return fwd_ws(nullptr, s).bytes;  // status + fp16 V (+ tile lists)
     case SPA2_OP_BWD: return bwd_ws(nullptr, s).bytes;
+    case SPA2_OP_BWD_CKPT: return ckpt_ws(nullptr, s).bytes;
   }
   return 0;
 }
@@ -428,6 +459,104 @@ spa2_status spa2_sparse_attn_bwd(const void* q, const void* k, const void* v, co
             w.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
             scale * 1.4426950408889634f, w.status, w.status + 32, g_wait_limit_ns, s.tiled ? 1 : 0,
             w.col_order};
+  SPA2_CUDA_TRY(launch_bwd(a, d, st));
+  return SPA2_OK;
+}
+
+spa2_status spa2_sparse_attn_fwd_ckpt(const void* q, const void* k, const void* v, int B, int H, int N, int d, int bq,
+                                      int bkv, const spa2_mask* mask, float softmax_scale, void* o, float* lse,
+                                      const spa2_pack8_tensor* q8, const spa2_pack8_tensor* k8,
+                                      const spa2_pack8_tensor* v8, void* ws, size_t ws_bytes, spa2_stream_t stream) {
+  Shape s;
+  spa2_status err;
+  if (!q || !k || !v || !o || !mask || !mask->row_cnt || !mask->row_idx || !packed_ok(q8) || !packed_ok(k8) ||
+      !packed_ok(v8))
+    return SPA2_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4))
+    return SPA2_ERR_INVALID_ARG;
+  if (!shape_ok(B, H, N, d, bq, bkv, &s, &err)) return err;
+  if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return SPA2_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256)) return SPA2_ERR_WORKSPACE;
+  FwdWs w = fwd_ws(ws, s);
+  if (ws_bytes < w.bytes) return SPA2_ERR_WORKSPACE;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)d);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  CUtensorMap tq, tk, tv, to;
+  if (!make_map(&tq, q, s, 128) || !make_map(&tk, k, s, 64) || !make_map(&tv, w.v16, s, 64, true) ||
+      !make_map(&to, o, s, 128))
+    return SPA2_ERR_CUDA;
+  SPA2_CUDA_TRY(cudaMemsetAsync(w.status, 0, 4, st));
+  const int* rc = mask->row_cnt;
+  const int* ri = mask->row_idx;
+  if (s.tiled) {
+    SPA2_CUDA_TRY(launch_tile_lists(mask->row_cnt, mask->row_idx, nullptr, nullptr, (int)s.BH, s.Tm, s.Tn, s.TMt,
+                                    s.TNt, s.bq, s.bkv, w.tiles.csr_cnt, w.tiles.csr_idx, nullptr, nullptr, w.status,
+                                    st));
+    rc = w.tiles.csr_cnt;
+    ri = w.tiles.csr_idx;
+  }
+  const long long rows = s.BH * s.N;
+  const spa2_pack8_tensor t[3] = {{const_cast<void*>(q), q8->codes, q8->exps, rows, d},
+                                  {const_cast<void*>(k), k8->codes, k8->exps, rows, d},
+                                  {const_cast<void*>(v), v8->codes, v8->exps, rows, d}};
+  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, false, st));
+  SPA2_CUDA_TRY(launch_v_to_f16(v, w.v16, rows * d, w.status, st));
+  FwdArgs a{&tq, &tk, &tv, &to, &to, 0, rc, ri, lse, (int)s.BH, s.N, s.TMt, s.TNt,
+            scale * 1.4426950408889634f, w.status, g_wait_limit_ns, s.tiled ? 1 : 0};
+  SPA2_CUDA_TRY(launch_fwd(a, d, st));
+  return SPA2_OK;
+}
+
+spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pack8_tensor* k8,
+                                      const spa2_pack8_tensor* v8, const void* dout, int B, int H, int N, int d,
+                                      int bq, int bkv, const spa2_mask* mask, float softmax_scale, void* dq, void* dk,
+                                      void* dv, int grad_dtype, void* ws, size_t ws_bytes, spa2_stream_t stream) {
+  Shape s;
+  spa2_status err;
+  if (!packed_ok(q8) || !packed_ok(k8) || !packed_ok(v8) || !dout || !dq || !dk || !dv || !mask || !mask->row_cnt ||
+      !mask->row_idx || !mask->col_cnt || !mask->col_idx)
+    return SPA2_ERR_INVALID_ARG;
+  if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16)) return SPA2_ERR_INVALID_ARG;
+  if (grad_dtype != SPA2_DTYPE_BF16 && grad_dtype != SPA2_DTYPE_F32) return SPA2_ERR_UNSUPPORTED;
+  if (!shape_ok(B, H, N, d, bq, bkv, &s, &err)) return err;
+  if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return SPA2_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256)) return SPA2_ERR_WORKSPACE;
+  CkptWs w = ckpt_ws(ws, s);
+  if (ws_bytes < w.bytes) return SPA2_ERR_WORKSPACE;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)d);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = grad_dtype == SPA2_DTYPE_F32;
+  CUtensorMap tq, tk, tv, tv16, to, tolo, tdo, tq16, tdq;
+  if (!make_map(&tq, w.q, s, 128) || !make_map(&tk, w.k, s, 64) || !make_map(&tv, w.v, s, 64) ||
+      !make_map(&tv16, w.v16, s, 64, true) || !make_map(&to, w.o, s, 128) || !make_map(&tolo, w.o_lo, s, 128) ||
+      !make_map(&tdo, w.b.do16, s, 128, true) || !make_map(&tq16, w.b.q16, s, 128, true) ||
+      !(f32 ? make_map_f32(&tdq, dq, s, 128) : make_map(&tdq, dq, s, 128)))
+    return SPA2_ERR_CUDA;
+  int* status = w.b.status;
+  SPA2_CUDA_TRY(cudaMemsetAsync(status, 0, 256, st));  // status word and the dK/dV column ticket
+  const int *rc = mask->row_cnt, *ri = mask->row_idx, *cc = mask->col_cnt, *ci = mask->col_idx;
+  if (s.tiled) {
+    const TileWs& t = w.b.tiles;
+    SPA2_CUDA_TRY(launch_tile_lists(mask->row_cnt, mask->row_idx, mask->col_cnt, mask->col_idx, (int)s.BH, s.Tm, s.Tn,
+                                    s.TMt, s.TNt, s.bq, s.bkv, t.csr_cnt, t.csr_idx, t.csc_cnt, t.csc_idx, status, st));
+    rc = t.csr_cnt;
+    ri = t.csr_idx;
+    cc = t.csc_cnt;
+    ci = t.csc_idx;
+  }
+  const long long rows = s.BH * s.N;
+  const spa2_pack8_tensor t[3] = {{w.q, q8->codes, q8->exps, rows, d},
+                                  {w.k, k8->codes, k8->exps, rows, d},
+                                  {w.v, v8->codes, v8->exps, rows, d}};
+  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, true, st));
+  SPA2_CUDA_TRY(launch_v_to_f16(w.v, w.v16, rows * d, status, st));
+  const float scale_log2 = scale * 1.4426950408889634f;
+  FwdArgs f{&tq, &tk, &tv16, &to, &tolo, 1, rc, ri, w.lse, (int)s.BH, s.N, s.TMt, s.TNt,
+            scale_log2, status, g_wait_limit_ns, s.tiled ? 1 : 0};
+  SPA2_CUDA_TRY(launch_fwd(f, d, st));
+  BwdArgs a{&tq, &tk, &tv, &tdo, &tq16, &tdq, w.q, w.k, w.o, w.o_lo, dout, w.v, w.lse, rc, ri, cc, ci, w.b.dvec,
+            w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale, scale_log2, status,
+            status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.b.col_order};
   SPA2_CUDA_TRY(launch_bwd(a, d, st));
   return SPA2_OK;
 }

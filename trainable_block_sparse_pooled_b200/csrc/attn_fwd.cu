@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(192, 2) fwd_kernel(const __grid_constant__ CUt
         }
       }
       const long long row = (long long)i * 128 + r;
-      if (row < N) lse[(long long)bh * N + row] = (m_use + log2f(l)) * 0.69314718055994530942f;
+      if (lse && row < N) lse[(long long)bh * N + row] = (m_use + log2f(l)) * 0.69314718055994530942f;
     }
     fence_proxy_async_smem();
     named_bar_sync(1, 128);

@@ -462,6 +462,26 @@ SPA2_DEV uint64_t f2_mul(uint64_t a, uint64_t b) {
 constexpr int TILE_ID_MASK = 0x3FFFFFFF;
 SPA2_DEV bool tile_excluded(int entry, int half) { return ((unsigned)entry >> (30 + half)) & 1u; }
 
+// ---------------------------------------------------------------------------
+// 8-bit groups (spa2_pack8). E is the biased fp32 exponent field of a group's
+// largest magnitude, so x * 2^(127 - E) lies in (-2, 2) and a code counts steps of
+// 2^(E - 133), 1/64 of that unit.
+// ---------------------------------------------------------------------------
+// 2^(127 - E); E = 254 needs an fp32 subnormal, which products here keep. For E =
+// 255 the codes do not matter.
+SPA2_DEV float pack8_scale(uint32_t E) { return __uint_as_float(E < 254u ? (254u - E) << 23 : 0x00400000u); }
+// rint(64 x scale) clamped to +-127: x scale is exact wherever it can reach a code
+// other than 0, and adding 1.5 * 2^23 rounds to the nearest integer, ties to even,
+// and leaves it in the low bits
+SPA2_DEV int8_t pack8_code(float x, float scale) {
+  const float y = fminf(fmaxf(x * scale, -1.984375f), 1.984375f);
+  return (int8_t)(__float_as_uint(fmaf(y, 64.f, 12582912.f)) & 0xffu);
+}
+// 2^(E - 133), below E = 7 an fp32 subnormal; NaN for E = 255
+SPA2_DEV float pack8_step(uint32_t E) {
+  return __uint_as_float(E >= 255u ? 0x7fffffffu : E >= 7u ? (E - 6u) << 23 : 1u << (16u + E));
+}
+
 SPA2_DEV float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

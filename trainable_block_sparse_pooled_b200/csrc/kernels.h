@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/spa2.h"
+
 namespace spa2 {
 
 // timing.cu: per-kernel event timing (spa2_timing_*). One id per kernel kind.
@@ -21,6 +23,9 @@ enum KernelId : int {
   KID_BWD_DQ,
   KID_PROBE,
   KID_TILES,
+  KID_ROTARY,
+  KID_PACK8,
+  KID_UNPACK8,
   KID_COUNT
 };
 
@@ -69,7 +74,7 @@ struct FwdArgs {
   int has_olo;
   const int* row_cnt;
   const int* row_idx;
-  float* lse;
+  float* lse;         // may be null
   int BH, N, Tm, Tn;
   float scale_log2;   // softmax_scale * log2(e)
   int* status;
@@ -115,6 +120,9 @@ struct BwdArgs {
   int* col_order;     // [BH * Tn]: the dK/dV pass's columns, head by head, long columns first (pre-pass)
 };
 cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s);
+
+// pack8.cu: 8-bit groups (checked arguments), x -> codes, exps or back
+cudaError_t launch_pack8(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, cudaStream_t s);
 
 // api.cu
 cudaError_t launch_timeout_probe(int* status, unsigned long long limit_ns, cudaStream_t s);

@@ -26,6 +26,9 @@ const char* const kNames[KID_COUNT] = {
     "bwd_dq_kernel",      // KID_BWD_DQ
     "timeout_probe_kernel",  // KID_PROBE
     "tile_list_kernel",   // KID_TILES
+    "rotary_kernel",      // KID_ROTARY
+    "pack8_kernel",       // KID_PACK8
+    "unpack8_kernel",     // KID_UNPACK8
 };
 
 struct Record {
