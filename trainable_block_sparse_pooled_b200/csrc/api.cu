@@ -499,8 +499,8 @@ spa2_status spa2_sparse_attn_fwd_ckpt(const void* q, const void* k, const void* 
   const spa2_pack8_tensor t[3] = {{const_cast<void*>(q), q8->codes, q8->exps, rows, d},
                                   {const_cast<void*>(k), k8->codes, k8->exps, rows, d},
                                   {const_cast<void*>(v), v8->codes, v8->exps, rows, d}};
-  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, false, st));
-  SPA2_CUDA_TRY(launch_v_to_f16(v, w.v16, rows * d, w.status, st));
+  void* const f16[3] = {nullptr, nullptr, w.v16};
+  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, false, st, f16, w.status));
   FwdArgs a{&tq, &tk, &tv, &to, &to, 0, rc, ri, lse, (int)s.BH, s.N, s.TMt, s.TNt,
             scale * 1.4426950408889634f, w.status, g_wait_limit_ns, s.tiled ? 1 : 0};
   SPA2_CUDA_TRY(launch_fwd(a, d, st));

@@ -482,6 +482,16 @@ SPA2_DEV float pack8_step(uint32_t E) {
   return __uint_as_float(E >= 255u ? 0x7fffffffu : E >= 7u ? (E - 6u) << 23 : 1u << (16u + E));
 }
 
+// (a, b) as an fp16 pair; |x| > 65504 (or NaN) is clamped and flagged
+SPA2_DEV uint32_t pack_f16_clamped(float a, float b, bool& bad) {
+  if (!(fabsf(a) <= 65504.f) || !(fabsf(b) <= 65504.f)) {
+    bad = true;
+    a = fminf(fmaxf(a, -65504.f), 65504.f);
+    b = fminf(fmaxf(b, -65504.f), 65504.f);
+  }
+  return pack_f16(a, b);
+}
+
 SPA2_DEV float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -121,8 +121,11 @@ struct BwdArgs {
 };
 cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s);
 
-// pack8.cu: 8-bit groups (checked arguments), x -> codes, exps or back
-cudaError_t launch_pack8(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, cudaStream_t s);
+// pack8.cu: 8-bit groups (checked arguments), x -> codes, exps or back. f16, where given, holds
+// for each tensor null or a place for an fp16 copy of x (of the values, unpacking), which
+// needs rows of whole 16-byte units; |x| > 65504 is clamped and reported to status.
+cudaError_t launch_pack8(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, cudaStream_t s,
+                         void* const* f16 = nullptr, int* status = nullptr);
 
 // api.cu
 cudaError_t launch_timeout_probe(int* status, unsigned long long limit_ns, cudaStream_t s);

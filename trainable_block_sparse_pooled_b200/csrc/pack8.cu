@@ -2,6 +2,14 @@
 // include/spa2.h): groups of 32 elements of a row share one exponent byte E, the
 // biased fp32 exponent of their largest magnitude; code = rint(x * 2^(133 - E)),
 // value = code * 2^(E - 133).
+//
+// Both kernels move bytes and little else (bf16: 3 + 1/32 bytes per element). Eight
+// elements of a row are a chunk (one 16-byte access, two for fp32), four chunks a group;
+// a thread takes UNROLL chunks, 256 apart, and loads them all before it works on the
+// first, so that enough of them are in flight to cover HBM's latency. The group's largest
+// exponent meets over two shuffles.
+// pack8_kernel, unpack8_kernel                rows that 16-byte accesses fit
+// pack8_single_kernel, unpack8_single_kernel  any others: one lane per element
 #include <algorithm>
 
 #include "common.cuh"
@@ -13,13 +21,154 @@ namespace {
 
 struct Pack8Args {
   spa2_pack8_tensor t[SPA2_PACK8_MAX];
+  uint32_t* f16[SPA2_PACK8_MAX];  // fp16 copy of the tensor (packing) or of its values, or null
+  int* status;                    // where |x| > 65504 is reported; needed for a copy
 };
+
+constexpr int CHUNK = 8, PER_GROUP = 4, UNROLL = 4, THREADS = 256;
+constexpr int PLACES = UNROLL * THREADS;  // chunk places of a block
+
+template <typename T>
+struct alignas(16) Chunk {
+  T e[CHUNK];
+};
+
+// The chunk places of a tensor are numbered row by row, whole groups to a row, so that the
+// last group of a row may hold places without a chunk. One thread's places of a block:
+template <bool FLAT>
+struct Places {
+  uint32_t per_row, first;
+  long long row0, base;
+
+  SPA2_DEV Places(const spa2_pack8_tensor& t) {
+    base = (long long)blockIdx.x * PLACES;
+    if (!FLAT) {
+      per_row = (uint32_t)((t.d + 31) / 32 * PER_GROUP);
+      row0 = base / per_row;
+      first = (uint32_t)(base - row0 * per_row);
+    }
+  }
+  // first element and group of place c (0 .. PLACES - 1); false where there is no chunk
+  SPA2_DEV bool at(const spa2_pack8_tensor& t, uint32_t c, long long& e, long long& group) const {
+    if (FLAT) {  // every row is whole groups
+      e = (base + c) * CHUNK;
+      group = (base + c) / PER_GROUP;
+      return e < t.rows * t.d;
+    }
+    const uint32_t p = first + c, r = p / per_row, col = p - r * per_row;
+    const long long row = row0 + r;
+    e = row * t.d + (long long)col * CHUNK;
+    group = row * (per_row / PER_GROUP) + col / PER_GROUP;
+    return row < t.rows && (long long)col * CHUNK < t.d;
+  }
+};
+
+SPA2_DEV float value_of(uint32_t bits, __nv_bfloat16) { return __uint_as_float(bits << 16); }
+SPA2_DEV float value_of(uint32_t bits, __half) { return __half2float(__ushort_as_half((unsigned short)bits)); }
+
+// largest magnitude's fp32 exponent field over a chunk, NaN and infinities being the largest
+template <typename T>
+SPA2_DEV uint32_t chunk_exponent(const Chunk<T>& x) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+  if constexpr (sizeof(T) == 2) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    return __float_as_uint(value_of(m, T())) >> 23;  // m has no sign
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m >> 23;
+  }
+}
 
 }  // namespace
 
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(THREADS) pack8_kernel(const __grid_constant__ Pack8Args a) {
+  pdl_trigger();
+  const spa2_pack8_tensor& t = a.t[blockIdx.y];
+  const Places<FLAT> places(t);
+  uint32_t* f16 = a.f16[blockIdx.y];
+  long long e[UNROLL], group[UNROLL];
+  bool here[UNROLL], bad = false;
+  Chunk<T> x[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    here[u] = places.at(t, u * THREADS + threadIdx.x, e[u], group[u]);
+    x[u] = Chunk<T>{};
+    if (here[u]) x[u] = *reinterpret_cast<const Chunk<T>*>(static_cast<const T*>(t.x) + e[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    uint32_t E = chunk_exponent(x[u]);
+    E = max(E, __shfl_xor_sync(0xffffffffu, E, 1));
+    E = max(E, __shfl_xor_sync(0xffffffffu, E, 2));
+    if (!here[u]) continue;
+    const float scale = pack8_scale(E);
+    union {
+      int8_t c[CHUNK];
+      uint2 w;
+    } code;
+    float f[CHUNK];
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) {
+      f[i] = static_cast<float>(x[u].e[i]);
+      code.c[i] = pack8_code(f[i], scale);
+    }
+    *reinterpret_cast<uint2*>(t.codes + e[u]) = code.w;
+    if (threadIdx.x % PER_GROUP == 0) t.exps[group[u]] = (uint8_t)E;
+    if (f16)
+      *reinterpret_cast<uint4*>(f16 + e[u] / 2) =
+          make_uint4(pack_f16_clamped(f[0], f[1], bad), pack_f16_clamped(f[2], f[3], bad),
+                     pack_f16_clamped(f[4], f[5], bad), pack_f16_clamped(f[6], f[7], bad));
+  }
+  if (bad) report(a.status, SPA2_ERR_RANGE);
+}
+
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(THREADS) unpack8_kernel(const __grid_constant__ Pack8Args a) {
+  const spa2_pack8_tensor& t = a.t[blockIdx.y];
+  const Places<FLAT> places(t);
+  uint32_t* f16 = a.f16[blockIdx.y];
+  long long e[UNROLL], group;
+  bool here[UNROLL], bad = false;
+  uint2 code[UNROLL];
+  uint8_t E[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    here[u] = places.at(t, u * THREADS + threadIdx.x, e[u], group);
+    if (here[u]) {
+      code[u] = *reinterpret_cast<const uint2*>(t.codes + e[u]);
+      E[u] = t.exps[group];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    if (!here[u]) continue;
+    const float step = pack8_step(E[u]);
+    float f[CHUNK];
+    Chunk<T> x;
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) {
+      const uint32_t w = i < 4 ? code[u].x : code[u].y;
+      f[i] = static_cast<float>((int8_t)(w >> (8 * (i & 3)))) * step;
+      x.e[i] = static_cast<T>(f[i]);
+    }
+    *reinterpret_cast<Chunk<T>*>(static_cast<T*>(t.x) + e[u]) = x;
+    if (f16)
+      *reinterpret_cast<uint4*>(f16 + e[u] / 2) =
+          make_uint4(pack_f16_clamped(f[0], f[1], bad), pack_f16_clamped(f[2], f[3], bad),
+                     pack_f16_clamped(f[4], f[5], bad), pack_f16_clamped(f[6], f[7], bad));
+  }
+  if (bad) report(a.status, SPA2_ERR_RANGE);
+}
+
 // one warp per group, one lane per element
 template <typename T>
-__global__ void __launch_bounds__(256) pack8_kernel(const Pack8Args a) {
+__global__ void __launch_bounds__(THREADS) pack8_single_kernel(const __grid_constant__ Pack8Args a) {
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
   const long long per_row = (t.d + 31) / 32, groups = t.rows * per_row;
   for (long long g = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); g < groups; g += (long long)gridDim.x * 8) {
@@ -32,7 +181,7 @@ __global__ void __launch_bounds__(256) pack8_kernel(const Pack8Args a) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) unpack8_kernel(const Pack8Args a) {
+__global__ void __launch_bounds__(THREADS) unpack8_single_kernel(const __grid_constant__ Pack8Args a) {
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
   const long long per_row = (t.d + 31) / 32, groups = t.rows * per_row;
   for (long long g = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); g < groups; g += (long long)gridDim.x * 8) {
@@ -45,20 +194,37 @@ __global__ void __launch_bounds__(256) unpack8_kernel(const Pack8Args a) {
 template <typename T>
 static cudaError_t launch_pack8_t(const Pack8Args& a, int n, bool unpack, cudaStream_t s) {
   long long groups = 0;
-  for (int i = 0; i < n; ++i) groups = std::max(groups, (long long)(a.t[i].rows * ((a.t[i].d + 31) / 32)));
+  bool chunks = true, flat = true;
+  for (int i = 0; i < n; ++i) {
+    const spa2_pack8_tensor& t = a.t[i];
+    groups = std::max(groups, (long long)(t.rows * ((t.d + 31) / 32)));
+    if (t.rows == 0) continue;
+    chunks &= t.d % CHUNK == 0 && t.d < (1LL << 31) && reinterpret_cast<uintptr_t>(t.x) % 16 == 0 &&
+              reinterpret_cast<uintptr_t>(t.codes) % CHUNK == 0;
+    flat &= t.d % SPA2_PACK8_GROUP == 0;
+  }
   if (groups == 0) return cudaSuccess;
-  const dim3 grid((unsigned)std::min((groups + 7) / 8, 1LL << 20), (unsigned)n);
   KernelTimer kt(unpack ? KID_UNPACK8 : KID_PACK8, s);
-  if (unpack)
-    unpack8_kernel<T><<<grid, 256, 0, s>>>(a);
-  else
-    pack8_kernel<T><<<grid, 256, 0, s>>>(a);
+  if (chunks) {
+    const dim3 grid((unsigned)((groups * PER_GROUP + PLACES - 1) / PLACES), (unsigned)n);
+    auto* k = unpack ? (flat ? unpack8_kernel<T, true> : unpack8_kernel<T, false>)
+                     : (flat ? pack8_kernel<T, true> : pack8_kernel<T, false>);
+    k<<<grid, THREADS, 0, s>>>(a);
+  } else {
+    const dim3 grid((unsigned)std::min((groups + 7) / 8, 1LL << 20), (unsigned)n);
+    (unpack ? unpack8_single_kernel<T> : pack8_single_kernel<T>)<<<grid, THREADS, 0, s>>>(a);
+  }
   return cudaGetLastError();
 }
 
-cudaError_t launch_pack8(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, cudaStream_t s) {
+cudaError_t launch_pack8(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, cudaStream_t s, void* const* f16,
+                         int* status) {
   Pack8Args a{};
-  for (int i = 0; i < n; ++i) a.t[i] = t[i];
+  for (int i = 0; i < n; ++i) {
+    a.t[i] = t[i];
+    a.f16[i] = f16 ? static_cast<uint32_t*>(f16[i]) : nullptr;
+  }
+  a.status = status;
   return dtype == SPA2_DTYPE_BF16  ? launch_pack8_t<__nv_bfloat16>(a, n, unpack, s)
          : dtype == SPA2_DTYPE_F16 ? launch_pack8_t<__half>(a, n, unpack, s)
                                    : launch_pack8_t<float>(a, n, unpack, s);

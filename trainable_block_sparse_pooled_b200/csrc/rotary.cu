@@ -1,7 +1,10 @@
 // Rotary positions (spa2_rotary in include/spa2.h): pairs of a head's row turned
 // by position * frequency, forward (angle theta) and backward (angle -theta).
 //
-// rotary_kernel  one thread per (token, pair or copied element) and head.
+// rotary_kernel  one thread per unit of a token's row (16 bytes, or 16 bytes and
+//                their partners), for all heads of the token or a run of them.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -26,22 +29,31 @@ struct RotaryArgs {
   float scale, sin_sign;
   long long tokens;   // B * N
   int N, d, rd;
+  // the launch: a unit is V elements turned in place, or (SPLIT) V and their V partners; the
+  // units of a row are `turned` such and then copied ones
+  int units, turned, step, partner;
+  int per_block;  // heads of a block
 };
 
 template <typename T>
-SPA2_DEV float to_f32(T x) { return static_cast<float>(x); }
-template <typename T>
-SPA2_DEV T from_f32(float x) { return static_cast<T>(x); }
+SPA2_DEV T from_f32(float x);
+template <>
+SPA2_DEV float from_f32<float>(float x) { return x; }
 template <>
 SPA2_DEV __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 template <>
 SPA2_DEV __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
+// V elements moved as one access
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Vec {
+  T e[V];
+};
+
 // cos and sin of position * inv_freq[p], both times the scale. The angle is
 // counted in turns and reduced to [-1/2, 1/2] in fp64 (a far position times a
 // frequency has more whole turns than fp32 has digits), then taken in fp32.
-SPA2_DEV float2 cos_sin(const RotaryArgs& a, long long token, int p) {
-  const long long b = token / a.N, n = token % a.N;
+SPA2_DEV float2 cos_sin(const RotaryArgs& a, int b, int n, int p) {
   int axis = 0;
 #pragma unroll
   for (int i = 1; i < SPA2_ROTARY_MAX_AXES; ++i) axis += p >= a.first[i];
@@ -56,45 +68,99 @@ SPA2_DEV float2 cos_sin(const RotaryArgs& a, long long token, int p) {
   return make_float2(c * a.scale, s * a.scale * a.sin_sign);
 }
 
-}  // namespace
-
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
-  const int units = a.rd / 2 + (a.d - a.rd);
-  const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (idx >= a.tokens * units) return;
-  const long long token = idx / units;
-  const int u = (int)(idx % units);
-  const long long b = token / a.N, n = token % a.N;
-  int h = blockIdx.y;
-  const RotaryTensor& t = a.t[h >= a.heads0];
-  if (h >= a.heads0) h -= a.heads0;
-  const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + h * t.xs[1] + n * t.xs[2];
-  T* y = static_cast<T*>(t.y) + b * t.ys[0] + h * t.ys[1] + n * t.ys[2];
-  if (u >= a.rd / 2) {
-    const int e = a.rd + u - a.rd / 2;
-    y[e] = x[e];
-    return;
-  }
-  const int i = HALF ? u : 2 * u, j = HALF ? u + a.rd / 2 : 2 * u + 1;
-  const float2 cs = cos_sin(a, token, u);
-  const float v = to_f32(x[i]), w = to_f32(x[j]);
-  y[i] = from_f32<T>(v * cs.x - w * cs.y);
-  y[j] = from_f32<T>(v * cs.y + w * cs.x);
+SPA2_DEV void turn(float x, float y, float2 cs, float& ox, float& oy) {
+  ox = x * cs.x - y * cs.y;
+  oy = x * cs.y + y * cs.x;
 }
 
-template <typename T>
-static cudaError_t launch_rotary(const RotaryArgs& a, int layout, cudaStream_t s) {
-  const long long threads = a.tokens * (a.rd / 2 + (a.d - a.rd));
-  const long long blocks = (threads + 255) / 256;
+}  // namespace
+
+template <typename T, int V, bool SPLIT>
+__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+  constexpr int PAIRS = SPLIT ? V : V / 2;  // pairs of a unit
+  constexpr int HB = SPLIT ? 2 : 4;         // heads in flight: 4 loads
+  using VT = Vec<T, V>;
+  const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long token = idx / a.units;
+  if (token >= a.tokens) return;
+  const int u = (int)(idx - token * a.units);
+  const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
+  const bool copy = u >= a.turned;
+  const int e0 = copy ? a.rd + (u - a.turned) * V : u * a.step;
+  const int e1 = e0 + a.partner;
+  float2 cs[PAIRS];
+  if (!copy) {
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) cs[i] = cos_sin(a, b, n, u * PAIRS + i);
+  }
+  const int h1 = min(a.heads, (int)(blockIdx.y + 1) * a.per_block);
+  for (int h = blockIdx.y * a.per_block; h < h1; h += HB) {
+    VT x[HB], z[HB];
+    T* y[HB];
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+      if (h + i < h1) {
+        const bool second = h + i >= a.heads0;
+        const RotaryTensor& t = a.t[second];
+        const int hh = h + i - (second ? a.heads0 : 0);
+        const T* from = static_cast<const T*>(t.x) + b * t.xs[0] + hh * t.xs[1] + n * t.xs[2];
+        y[i] = static_cast<T*>(t.y) + b * t.ys[0] + hh * t.ys[1] + n * t.ys[2];
+        x[i] = *reinterpret_cast<const VT*>(from + e0);
+        if (SPLIT && !copy) z[i] = *reinterpret_cast<const VT*>(from + e1);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < HB; ++i) {
+      if (h + i < h1) {
+        if (!copy) {
+#pragma unroll
+          for (int p = 0; p < PAIRS; ++p) {
+            T& s = x[i].e[SPLIT ? p : 2 * p];
+            T& t = SPLIT ? z[i].e[p] : x[i].e[2 * p + 1];
+            float v, w;
+            turn(static_cast<float>(s), static_cast<float>(t), cs[p], v, w);
+            s = from_f32<T>(v);
+            t = from_f32<T>(w);
+          }
+          if (SPLIT) *reinterpret_cast<VT*>(y[i] + e1) = z[i];
+        }
+        *reinterpret_cast<VT*>(y[i] + e0) = x[i];
+      }
+    }
+  }
+}
+
+template <typename T, int V, bool SPLIT>
+static cudaError_t launch_rotary(RotaryArgs a, bool half, cudaStream_t s) {
+  a.step = SPLIT && !half ? 2 : V;
+  a.partner = half ? a.rd / 2 : 1;
+  a.turned = a.rd / (SPLIT ? 2 * V : V);
+  a.units = a.turned + (a.d - a.rd) / V;
+  const long long blocks = (a.tokens * a.units + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks, (unsigned)a.heads);
+  // one block takes all heads of its tokens, so that angles are computed once; with few
+  // tokens the heads are split over blocks until there are about 8 for every SM
+  const long long split = std::min<long long>((a.heads + 3) / 4, std::max<long long>(1, 1184 / blocks));
+  a.per_block = (int)((a.heads + split - 1) / split);
+  const dim3 grid((unsigned)blocks, (unsigned)((a.heads + a.per_block - 1) / a.per_block));
   KernelTimer kt(KID_ROTARY, s);
-  if (layout == SPA2_ROTARY_HALF)
-    rotary_kernel<T, true><<<grid, 256, 0, s>>>(a);
-  else
-    rotary_kernel<T, false><<<grid, 256, 0, s>>>(a);
+  rotary_kernel<T, V, SPLIT><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+// the widest access that all rows allow: 16 bytes, 8 bytes or single elements
+template <typename T>
+static cudaError_t launch_rotary_t(const RotaryArgs& a, int n, bool half, cudaStream_t s) {
+  uint64_t all = (uint64_t)(half ? a.rd / 2 : a.rd) | (uint64_t)(a.d - a.rd);  // in elements
+  for (int i = 0; i < n; ++i) {
+    all |= reinterpret_cast<uintptr_t>(a.t[i].x) / sizeof(T) | reinterpret_cast<uintptr_t>(a.t[i].y) / sizeof(T);
+    for (int j = 0; j < 3; ++j) all |= (uint64_t)a.t[i].xs[j] | (uint64_t)a.t[i].ys[j];
+  }
+  constexpr int W = 16 / sizeof(T);
+  if (all % W == 0) return half ? launch_rotary<T, W, true>(a, half, s) : launch_rotary<T, W, false>(a, half, s);
+  if (all % (W / 2) == 0)
+    return half ? launch_rotary<T, W / 2, true>(a, half, s) : launch_rotary<T, W / 2, false>(a, half, s);
+  return launch_rotary<T, 1, true>(a, half, s);
 }
 
 }  // namespace spa2
@@ -154,9 +220,10 @@ spa2_status spa2_rotary(const spa2_rotary_tensor* t, int n, int B, int N, int d,
   if (heads > 65535) return SPA2_ERR_UNSUPPORTED;
   a.heads = (int)heads;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == SPA2_DTYPE_BF16  ? launch_rotary<__nv_bfloat16>(a, spec->layout, s)
-                        : dtype == SPA2_DTYPE_F16 ? launch_rotary<__half>(a, spec->layout, s)
-                                                  : launch_rotary<float>(a, spec->layout, s);
+  const bool half = spec->layout == SPA2_ROTARY_HALF;
+  const cudaError_t e = dtype == SPA2_DTYPE_BF16  ? launch_rotary_t<__nv_bfloat16>(a, n, half, s)
+                        : dtype == SPA2_DTYPE_F16 ? launch_rotary_t<__half>(a, n, half, s)
+                                                  : launch_rotary_t<float>(a, n, half, s);
   return e == cudaSuccess ? SPA2_OK : SPA2_ERR_CUDA;
 }
 
