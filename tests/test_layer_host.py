@@ -75,7 +75,7 @@ def test_axial_and_grid_refusals():
 # ---- refusals of the front ends ---------------------------------------------------
 def _spec(B=2, N=5, d=8, device="cpu", **kw):
     kw.setdefault("inv_freq", torch.ones(4, dtype=torch.float64))
-    return rotary._spec(rotary.Rotary(**kw), B, N, d, torch.device(device))
+    return b.spa2_rotary_spec.from_buffer_copy(rotary._spec(rotary.Rotary(**kw), B, N, d, torch.device(device))[0])
 
 
 def test_rotary_spec_marshalling():

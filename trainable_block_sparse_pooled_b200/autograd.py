@@ -51,6 +51,10 @@ class _StatusWatch:
     def __init__(self, spa: b.Spa2):
         self.spa = spa
         self.host = torch.zeros(self.SLOTS, 3, dtype=torch.int32).pin_memory()
+        self.codes = self.host.numpy()
+        self.places = [[self.host[i, j:j + 1] for j in range(3)] for i in range(self.SLOTS)]
+        self.words: dict = {}              # op -> its status word on the device
+        self.events: list = [None] * self.SLOTS
         self.pending: deque = deque()      # (slot, event, ops) in launch order
         self.next = 0
 
@@ -60,9 +64,14 @@ class _StatusWatch:
             self._finish(self.pending.popleft(), wait=True)
         slot = self.next
         self.next = (self.next + 1) % self.SLOTS
-        for col, op in enumerate(ops):
-            self.host[slot, col:col + 1].copy_(self.spa.ws[op][:4].view(torch.int32), non_blocking=True)
-        ev = torch.cuda.Event()
+        for place, op in zip(self.places[slot], ops):
+            word = self.words.get(op)
+            if word is None:
+                word = self.words[op] = self.spa.ws[op][:4].view(torch.int32)
+            place.copy_(word, non_blocking=True)
+        ev = self.events[slot]
+        if ev is None:
+            ev = self.events[slot] = torch.cuda.Event()
         ev.record()
         self.pending.append((slot, ev, tuple(ops)))
 
@@ -81,7 +90,7 @@ class _StatusWatch:
         if wait:
             ev.synchronize()
         for col, op in enumerate(ops):
-            code = int(self.host[slot, col])
+            code = int(self.codes[slot, col])
             if code != b.OK:
                 self.pending.clear()
                 raise b.Spa2Error(code, f"device status of sparse_attention (op {op})")
@@ -104,8 +113,8 @@ def _spa(B, H, N, d, device, bq=b.BQ, bkv=b.BKV) -> b.Spa2:
         s = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv)
         s.watch = _NoWatch()
         return s
-    stream = torch.cuda.current_stream(device).cuda_stream
-    key = (B, H, N, d, bq, bkv, str(device), stream)
+    index = torch.cuda.current_device() if device.index is None else device.index
+    key = (B, H, N, d, bq, bkv, index, torch._C._cuda_getCurrentRawStream(index))
     s = _cache.get(key)
     if s is None:
         s = _cache[key] = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv)
@@ -171,50 +180,42 @@ class CheckpointedAttentionFunction(torch.autograd.Function):
     same o, and the gradients of the attention at the kept values."""
 
     @staticmethod
-    def forward(ctx, q, k, v, k_frac: float, p_frac: float, scale: float, mask: b.Mask | None, bq: int, bkv: int):
+    def forward(ctx, q, k, v, scale: float, mask: b.Mask, bq: int, bkv: int):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        B, H, N, d = q.shape
-        s = _spa(B, H, N, d, q.device, bq, bkv)
-        ops = [b.OP_FWD]
-        if mask is None:
-            mask = s.block_mask(q, k, k_frac, p_frac)
-            ops.insert(0, b.OP_MASK)
+        s = _spa(*q.shape, q.device, bq, bkv)
         o, kept = s.fwd_ckpt(q, k, v, mask, scale)
-        s.watch.after(ops)
-        ctx.save_for_backward(*(p.data for p in kept))
+        s.watch.after((b.OP_FWD,))
+        ctx.save_for_backward(*[p.data for p in kept])
         ctx.mask, ctx.scale, ctx.blocks = mask, scale, (bq, bkv)
-        row_cnt = mask.row_cnt.clone()  # the kept-block counts (a copy: a reused mask serves many calls)
-        ctx.mark_non_differentiable(row_cnt)
-        return o, row_cnt
+        return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, do, _row_cnt_grad):
-        B, H, N, d = do.shape
-        s = _spa(B, H, N, d, do.device, *ctx.blocks)
-        kept = tuple(Packed(data, do.shape, do.dtype) for data in ctx.saved_tensors)
-        dq, dk, dv = s.bwd_ckpt(kept, do.contiguous(), ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
-        s.watch.after([b.OP_BWD_CKPT])
-        return dq, dk, dv, None, None, None, None, None, None
+    def backward(ctx, do):
+        shape, dtype = do.shape, do.dtype
+        s = _spa(*shape, do.device, *ctx.blocks)
+        kept = [Packed(data, shape, dtype) for data in ctx.saved_tensors]
+        grads = s.bwd_ckpt(kept, do.contiguous(), ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
+        s.watch.after((b.OP_BWD_CKPT,))
+        return (*grads, None, None, None, None)
 
 
 def _check_attention(q, k, v, mask, bq, bkv):
     """What the checkpointed call checks before it touches the device."""
-    if any(x.dtype != torch.bfloat16 for x in (q, k, v)):
+    if not q.dtype == k.dtype == v.dtype == torch.bfloat16:
         raise TypeError("sparse_attention expects bf16 q, k, v")
-    if q.dim() != 4 or k.shape != q.shape or v.shape != q.shape:
+    shape, device = q.shape, q.device
+    if len(shape) != 4 or k.shape != shape or v.shape != shape:
         raise ValueError("sparse_attention expects q, k, v of one shape [B, H, N, d]")
-    if any(x.device != q.device or x.device.type != "cuda" for x in (q, k, v)):
+    if device.type != "cuda" or k.device != device or v.device != device:
         raise ValueError("sparse_attention expects q, k, v on one CUDA device")
     if mask is not None:
-        B, H, N, _ = q.shape
+        B, H, N, _ = shape
         Tm, Tn = b.block_counts(N, bq, bkv)
-        want = {"row_cnt": (B, H, Tm), "row_idx": (B, H, Tm, Tn), "col_cnt": (B, H, Tn), "col_idx": (B, H, Tn, Tm)}
-        for name, shape in want.items():
-            t = getattr(mask, name)
-            if t is None or tuple(t.shape) != shape or t.device != q.device or t.dtype != torch.int32 \
-                    or not t.is_contiguous():
-                raise ValueError("mask does not belong to a problem of this shape and device")
+        for t, want in ((mask.row_cnt, (B, H, Tm)), (mask.row_idx, (B, H, Tm, Tn)), (mask.col_cnt, (B, H, Tn)),
+                        (mask.col_idx, (B, H, Tn, Tm))):
+            if t is None or t.shape != want or t.device != device or t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("mask must be int32 lists, contiguous, of a problem of this shape and device")
 
 
 def block_mask(q, k, k_frac: float, p_frac: float, bq: int = b.BQ, bkv: int = b.BKV) -> b.Mask:
@@ -251,11 +252,14 @@ def sparse_attention(q, k, v, k_frac: float = 0.0, p_frac: float = 0.0, scale: f
     if rotary is not None:
         q, k = apply_rotary(q, k, inv_freq=rotary.inv_freq, positions=rotary.positions, layout=rotary.layout,
                             axes=rotary.axes, scale=rotary.scale)
-    function = SparseAttentionFunction
-    if checkpoint is not None:
-        _check_attention(q, k, v, mask, bq, bkv)
-        if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-            function = CheckpointedAttentionFunction
     with b.on_device(q.device):
-        o, row_cnt = function.apply(q, k, v, k_frac, p_frac, scale, mask, bq, bkv)
+        if checkpoint is not None:
+            _check_attention(q, k, v, mask, bq, bkv)
+            if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+                if mask is None:
+                    q, k = q.contiguous(), k.contiguous()  # once for both
+                    mask = block_mask(q, k, k_frac, p_frac, bq, bkv)
+                o = CheckpointedAttentionFunction.apply(q, k, v, scale, mask, bq, bkv)
+                return (o, mask.row_cnt.clone()) if return_mask else o
+        o, row_cnt = SparseAttentionFunction.apply(q, k, v, k_frac, p_frac, scale, mask, bq, bkv)
     return (o, row_cnt) if return_mask else o

@@ -15,6 +15,7 @@ import ctypes
 import math
 import os
 import re
+import struct
 from dataclasses import dataclass
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -103,10 +104,11 @@ _SIGS = {
     "spa2_sparse_attn_bwd": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 6
                              + [ctypes.POINTER(spa2_mask), ctypes.c_float] + [ctypes.c_void_p] * 3
                              + [ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
-    "spa2_rotary": (ctypes.c_int, [ctypes.POINTER(spa2_rotary_tensor)] + [ctypes.c_int] * 5
-                    + [ctypes.POINTER(spa2_rotary_spec), ctypes.c_int, ctypes.c_void_p]),
-    "spa2_pack8": (ctypes.c_int, [ctypes.POINTER(spa2_pack8_tensor), ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
-    "spa2_unpack8": (ctypes.c_int, [ctypes.POINTER(spa2_pack8_tensor), ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    # structures as void*: taken as ctypes objects or as their bytes
+    "spa2_rotary": (ctypes.c_int, [ctypes.c_void_p] + [ctypes.c_int] * 5
+                    + [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
+    "spa2_pack8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "spa2_unpack8": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
     "spa2_sparse_attn_fwd_ckpt": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int] * 6
                                   + [ctypes.POINTER(spa2_mask), ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]
                                   + [ctypes.POINTER(spa2_pack8_tensor)] * 3
@@ -190,6 +192,23 @@ def spa2_sparse_attn_bwd(q, k, v, o, o_lo, lse, dout, B, H, N, d, bq, bkv, mask:
                          grad_dtype, ws, ws_bytes, stream) -> int:
     return lib().spa2_sparse_attn_bwd(q, k, v, o, o_lo, lse, dout, B, H, N, d, bq, bkv, ctypes.byref(mask), scale,
                                       dq, dk, dv, grad_dtype, ws, ws_bytes, stream)
+
+
+# The structures' bytes, which struct packs several times as fast as ctypes fills fields
+# (a call of a few tokens is mostly the host's time).
+_ROTARY_SPEC = struct.Struct("@Pi3q5iP2if0q")
+_ROTARY_TENSOR = "PPi6q"
+_PACK8_TENSOR = "PPPqq"
+ROTARY_TENSORS = (None, struct.Struct("@" + _ROTARY_TENSOR), struct.Struct("@" + 2 * _ROTARY_TENSOR))
+PACK8_TENSORS = tuple(struct.Struct("@" + n * _PACK8_TENSOR) for n in range(PACK8_MAX + 1))
+assert _ROTARY_SPEC.size == ctypes.sizeof(spa2_rotary_spec) and PACK8_TENSORS[1].size == ctypes.sizeof(spa2_pack8_tensor)
+assert ROTARY_TENSORS[2].size == 2 * ctypes.sizeof(spa2_rotary_tensor)
+
+
+def rotary_spec(positions, position_bytes, position_stride, pairs, inv_freq, rotary_dim, layout, scale) -> bytes:
+    """A spa2_rotary_spec as bytes: pointers (or None), strides (batch, axis, token), the pairs of each axis."""
+    return _ROTARY_SPEC.pack(positions or 0, position_bytes, *position_stride, len(pairs),
+                             *pairs, *(0,) * (ROTARY_MAX_AXES - len(pairs)), inv_freq, rotary_dim, layout, scale)
 
 
 def spa2_rotary(tensors, B, N, d, dtype, spec: spa2_rotary_spec, inverse, stream) -> int:
@@ -278,7 +297,7 @@ def block_counts(N: int, bq: int = BQ, bkv: int = BKV) -> tuple[int, int]:
 
 
 def _stream(torch):
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def on_device(device):
@@ -388,7 +407,7 @@ class Spa2:
         """dQ, dK, dV at the values of the checkpoints `kept` (from fwd_ckpt or checkpoint.pack8)."""
         t = self.torch
         gt = t.float32 if grad_dtype == DTYPE_F32 else t.bfloat16
-        dq, dk, dv = (t.empty(self.B, self.H, self.N, self.d, dtype=gt, device=dout.device) for _ in range(3))
+        dq, dk, dv = (t.empty_like(dout, dtype=gt) for _ in range(3))
         cm = mask.c()
         ws = self._ckpt_ws()
         _check(spa2_sparse_attn_bwd_ckpt(*(p.c() for p in kept), dout.data_ptr(), self.B, self.H, self.N, self.d,

@@ -36,14 +36,15 @@ class Packed:
 
     @staticmethod
     def _sizes(shape):
-        d = shape[-1]
-        n = shape.numel()
-        return n, -(-n // 16) * 16, (n // d) * -(-d // b.PACK8_GROUP) if n else 0
+        """(elements, byte at which the exponents begin, exponents)"""
+        d, n = shape[-1], shape.numel()
+        return n, (n + 15) & ~15, n // d * ((d + 31) >> 5)
 
     @classmethod
     def empty_like(cls, x: torch.Tensor) -> "Packed":
-        _, at, groups = cls._sizes(x.shape)
-        return cls(torch.empty(at + groups, dtype=torch.uint8, device=x.device), x.shape, x.dtype)
+        shape = x.shape
+        _, at, groups = cls._sizes(shape)
+        return cls(torch.empty(at + groups, dtype=torch.uint8, device=x.device), shape, x.dtype)
 
     @property
     def codes(self) -> torch.Tensor:
@@ -60,49 +61,60 @@ class Packed:
     def nbytes(self) -> int:
         return self.data.numel()
 
-    def c(self, x: torch.Tensor | None = None) -> b.spa2_pack8_tensor:
+    def fields(self, x: torch.Tensor | None = None) -> tuple:
+        """The fields of a spa2_pack8_tensor of this checkpoint and x (contiguous, of its shape)."""
         n, at, _ = self._sizes(self.shape)
         p, d = self.data.data_ptr(), self.shape[-1]
-        return b.spa2_pack8_tensor(None if x is None else x.data_ptr(), p, p + at, n // d, d)
+        return 0 if x is None else x.data_ptr(), p, p + at, n // d, d
+
+    def c(self, x: torch.Tensor | None = None) -> b.spa2_pack8_tensor:
+        return b.spa2_pack8_tensor(*self.fields(x))
 
 
 def _launch(call, items, dtype, device, what):
     """`items`: (Packed, tensor) pairs, at most PACK8_MAX to a launch, on the device's current stream."""
     with b.on_device(device):
-        s = torch.cuda.current_stream().cuda_stream
+        s = b._stream(torch)
         for i in range(0, len(items), b.PACK8_MAX):
             part = items[i:i + b.PACK8_MAX]
-            b._check(call((b.spa2_pack8_tensor * len(part))(*(p.c(x) for p, x in part)), _DTYPES[dtype], s), what)
-
-
-def _same(items, what):
-    if not items:
-        raise ValueError(f"{what} expects at least one tensor")
-    first = items[0]
-    if any(x.dtype != first.dtype for x in items):
-        raise TypeError(f"{what} expects tensors of one dtype")
+            fields = [f for p, x in part for f in p.fields(x)]
+            rc = call(b.PACK8_TENSORS[len(part)].pack(*fields), len(part), _DTYPES[dtype], s)
+            if rc != b.OK:
+                raise b.Spa2Error(rc, what)
 
 
 def pack8(*xs: torch.Tensor) -> tuple[Packed, ...]:
     """8-bit checkpoints of CUDA tensors of one dtype (bf16, fp16 or fp32) and any shapes."""
-    _same(xs, "pack8")
-    if xs[0].dtype not in _DTYPES:
-        raise TypeError(f"pack8 expects bf16, fp16 or fp32 tensors, got {xs[0].dtype}")
-    if any(x.device != xs[0].device or x.device.type != "cuda" for x in xs):
-        raise ValueError("pack8 expects tensors on one CUDA device")
-    if any(x.dim() < 1 or x.shape[-1] < 1 for x in xs):
-        raise ValueError("pack8 expects tensors of at least one dimension, the last of them not empty")
-    items = [(Packed.empty_like(x), x.detach().contiguous()) for x in xs]
-    _launch(b.spa2_pack8, items, xs[0].dtype, xs[0].device, "spa2_pack8")
-    return tuple(p for p, _ in items)
+    if not xs:
+        raise ValueError("pack8 expects at least one tensor")
+    dtype, device = xs[0].dtype, xs[0].device
+    if dtype not in _DTYPES:
+        raise TypeError(f"pack8 expects bf16, fp16 or fp32 tensors, got {dtype}")
+    for x in xs:
+        if x.dtype != dtype:
+            raise TypeError("pack8 expects tensors of one dtype")
+    items = []
+    for x in xs:
+        if x.device != device or device.type != "cuda":
+            raise ValueError("pack8 expects tensors on one CUDA device")
+        if x.dim() < 1 or x.shape[-1] < 1:
+            raise ValueError("pack8 expects tensors of at least one dimension, the last of them not empty")
+        items.append((Packed.empty_like(x), x if x.is_contiguous() else x.detach().contiguous()))
+    _launch(b.lib().spa2_pack8, items, dtype, device, "spa2_pack8")
+    return tuple([p for p, _ in items])
 
 
 def unpack8(*packed: Packed) -> tuple[torch.Tensor, ...]:
     """The kept values of each checkpoint, contiguous, in its tensor's shape and dtype."""
-    _same(packed, "unpack8")
-    device = packed[0].data.device
-    if any(p.data.device != device for p in packed):
-        raise ValueError("unpack8 expects checkpoints on one CUDA device")
-    items = [(p, torch.empty(p.shape, dtype=p.dtype, device=device)) for p in packed]
-    _launch(b.spa2_unpack8, items, packed[0].dtype, device, "spa2_unpack8")
-    return tuple(x for _, x in items)
+    if not packed:
+        raise ValueError("unpack8 expects at least one checkpoint")
+    dtype, device = packed[0].dtype, packed[0].data.device
+    for p in packed:
+        if p.dtype != dtype:
+            raise TypeError("unpack8 expects checkpoints of tensors of one dtype")
+    for p in packed:
+        if p.data.device != device or device.type != "cuda":
+            raise ValueError("unpack8 expects checkpoints on one CUDA device")
+    items = [(p, torch.empty(p.shape, dtype=dtype, device=device)) for p in packed]
+    _launch(b.lib().spa2_unpack8, items, dtype, device, "spa2_unpack8")
+    return tuple([x for _, x in items])

@@ -103,81 +103,78 @@ class Rotary:
     scale: float = 1.0
 
 
-def _spec(r: Rotary, B: int, N: int, d: int, device) -> b.spa2_rotary_spec:
-    f = r.inv_freq
-    if r.layout not in _LAYOUTS:
+def _spec(r: Rotary, B: int, N: int, d: int, device) -> tuple:
+    """(spa2_rotary_spec as bytes, the tensors it points into) of r for q and k [B, H, N, d]."""
+    f, pos = r.inv_freq, r.positions
+    layout = _LAYOUTS.get(r.layout)
+    if layout is None:
         raise ValueError(f"unknown layout {r.layout!r}: 'interleaved' or 'half'")
     if f.dtype != torch.float64 or f.dim() != 1:
         raise TypeError("inv_freq must be a float64 tensor of one dimension")
-    pairs = f.numel()
+    pairs = f.shape[0]
     if pairs < 1 or 2 * pairs > d:
         raise ValueError(f"inv_freq has {pairs} frequencies: between 1 and d / 2 = {d // 2} are wanted")
     axes = (pairs,) if r.axes is None else tuple(r.axes)
-    if not 1 <= len(axes) <= b.ROTARY_MAX_AXES or min(axes) < 0 or sum(axes) != pairs:
+    n_axes = len(axes)
+    if not 1 <= n_axes <= b.ROTARY_MAX_AXES or min(axes) < 0 or sum(axes) != pairs:
         raise ValueError(f"axes {axes} must be 1 to {b.ROTARY_MAX_AXES} pair counts with sum {pairs}")
     if not math.isfinite(r.scale):
         raise ValueError("scale must be finite")
-    pos, stride = r.positions, (0, 0, 0)
+    at, size, stride = None, 8, (0, 0, 0)
     if pos is None:
-        if len(axes) != 1:
+        if n_axes != 1:
             raise ValueError("more than one axis needs positions")
     else:
-        if pos.dtype not in (torch.int32, torch.int64):
+        if pos.dtype == torch.int32:
+            size = 4
+        elif pos.dtype != torch.int64:
             raise TypeError("positions must be int32 or int64")
-        want = (N,) if len(axes) == 1 else (len(axes), N)
-        if tuple(pos.shape) == want:
-            batch = 0
-        elif tuple(pos.shape) == (B, *want):
-            batch = pos.stride(0)
+        want = (N,) if n_axes == 1 else (n_axes, N)
+        shape, st = tuple(pos.shape), pos.stride()
+        if shape == want:
+            stride = (0, st[0] if n_axes > 1 else 0, st[-1])
+        elif shape == (B, *want):
+            stride = (st[0], st[1] if n_axes > 1 else 0, st[-1])
         else:
-            raise ValueError(f"positions have shape {tuple(pos.shape)}: {want} or {(B, *want)} is wanted")
-        stride = (batch, pos.stride(-2) if len(axes) > 1 else 0, pos.stride(-1))
-    if f.device != device or (pos is not None and pos.device != device):
-        raise ValueError("inv_freq and positions must be on the device of q")
+            raise ValueError(f"positions have shape {shape}: {want} or {(B, *want)} is wanted")
+        if pos.device != device:
+            raise ValueError("positions must be on the device of q")
+        at = pos.data_ptr()
+    if f.device != device:
+        raise ValueError("inv_freq must be on the device of q")
     if f.stride(0) != 1:
         f = f.contiguous()
-    s = b.spa2_rotary_spec()
-    s.positions = None if pos is None else pos.data_ptr()
-    s.position_bytes = 8 if pos is None else pos.element_size()
-    s.position_stride[:] = stride
-    s.axes = len(axes)
-    s.pairs[:len(axes)] = axes
-    s.inv_freq, s.rotary_dim, s.layout, s.scale = f.data_ptr(), 2 * pairs, _LAYOUTS[r.layout], r.scale
-    s.keep = f  # the call below reads it on the current stream
-    return s
-
-
-def _check_inputs(xs):
-    q = xs[0]
-    if any(x.dtype not in _DTYPES for x in xs):
-        raise TypeError("apply_rotary expects bf16, fp16 or fp32 tensors")
-    if any(x.dtype != q.dtype for x in xs):
-        raise TypeError("q and k must have one dtype")
-    if any(x.dim() != 4 for x in xs):
-        raise ValueError("apply_rotary expects [B, H, N, d] tensors")
-    if any(x.device != q.device or x.device.type != "cuda" for x in xs):
-        raise ValueError("apply_rotary expects tensors on one CUDA device")
-    if any((x.shape[0], x.shape[2], x.shape[3]) != (q.shape[0], q.shape[2], q.shape[3]) for x in xs):
-        raise ValueError("q and k must agree in batch, length and head width")
+    return b.rotary_spec(at, size, stride, axes, f.data_ptr(), 2 * pairs, layout, r.scale), f
 
 
 def _turn(xs, outs, r: Rotary, inverse: bool):
     """outs[i] <- xs[i] turned; every tensor [B, H, N, d] with a contiguous last dimension."""
-    B, _, N, d = xs[0].shape
-    spec = _spec(r, B, N, d, xs[0].device)
-    pairs = [(x, y) for x, y in zip(xs, outs) if x.numel()]
-    if not pairs:
+    x = xs[0]
+    B, _, N, d = x.shape
+    device = x.device
+    spec, keep = _spec(r, B, N, d, device)  # keep: what the call reads on the current stream
+    fields = []
+    for x, y in zip(xs, outs):
+        heads = x.shape[1]
+        if B and heads and N:
+            fields += x.data_ptr(), y.data_ptr(), heads, *x.stride()[:3], *y.stride()[:3]
+    n = len(fields) // 9
+    if n == 0:
         return
-    t = (b.spa2_rotary_tensor * len(pairs))()
-    for e, (x, y) in zip(t, pairs):
-        e.x, e.y, e.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
-        e.x_stride[:], e.y_stride[:] = x.stride()[:3], y.stride()[:3]
-    with b.on_device(xs[0].device):
-        b._check(b.spa2_rotary(t, B, N, d, _DTYPES[xs[0].dtype], spec, inverse, b._stream(torch)), "spa2_rotary")
+    with b.on_device(device):
+        rc = b.lib().spa2_rotary(b.ROTARY_TENSORS[n].pack(*fields), n, B, N, d, _DTYPES[x.dtype], spec, inverse,
+                                 b._stream(torch))
+    if rc != b.OK:
+        raise b.Spa2Error(rc, "spa2_rotary")
 
 
-def _rows(x):
-    return x if x.stride(-1) == 1 or x.shape[-1] == 1 else x.contiguous()
+def _turned(r: Rotary, inverse: bool, strides, xs):
+    """xs turned, each in strides of its own or (None) contiguous."""
+    xs = [x if x.stride(-1) == 1 or x.shape[-1] == 1 else x.contiguous() for x in xs]
+    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) if st is None else
+            torch.empty_strided(x.shape, st, dtype=x.dtype, device=x.device) for x, st in zip(xs, strides)]
+    _turn(xs, outs, r, inverse)
+    return outs
 
 
 class RotaryFunction(torch.autograd.Function):
@@ -187,29 +184,33 @@ class RotaryFunction(torch.autograd.Function):
     def forward(ctx, r: Rotary, inverse: bool, strides, *xs):
         ctx.save_for_backward(r.inv_freq, r.positions)  # so that a change in between is noticed
         ctx.spec, ctx.inverse = (r.layout, r.axes, r.scale), inverse
-        ctx.strides = [(x.shape, x.stride()) for x in xs]
+        ctx.strides = [_dense(x) for x in xs]
         ctx.set_materialize_grads(False)
-        xs = [_rows(x) for x in xs]
-        outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) if st is None else
-                torch.empty_strided(*st, dtype=x.dtype, device=x.device) for x, st in zip(xs, strides)]
-        _turn(xs, outs, r, inverse)
-        return tuple(outs)
+        return tuple(_turned(r, inverse, strides, xs))
 
     @staticmethod
     def backward(ctx, *grads):
-        at = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[3 + i]]
+        wanted = ctx.needs_input_grad
+        at = [i for i, g in enumerate(grads) if g is not None and wanted[3 + i]]
         out = [None] * len(grads)
         if at:
-            turned = RotaryFunction.apply(Rotary(*ctx.saved_tensors, *ctx.spec), not ctx.inverse, [_dense(*ctx.strides[i]) for i in at],
-                                          *(grads[i] for i in at))
+            r = Rotary(*ctx.saved_tensors, *ctx.spec)
+            strides, xs = [ctx.strides[i] for i in at], [grads[i] for i in at]
+            if torch.is_grad_enabled():  # the gradient will be differentiated itself
+                turned = RotaryFunction.apply(r, not ctx.inverse, strides, *xs)
+            else:
+                turned = _turned(r, not ctx.inverse, strides, xs)
             for i, g in zip(at, turned):
                 out[i] = g
         return (None, None, None, *out)
 
 
-def _dense(shape, stride):
-    """(shape, strides without gaps in the order of `stride`), None (contiguous) where that has broadcast dimensions
-    or the last one is not innermost."""
+def _dense(x):
+    """Strides without gaps in the order of x's, or None (contiguous) where x has broadcast dimensions or its
+    last dimension is not innermost."""
+    shape, stride = x.shape, x.stride()
+    if x.is_contiguous():
+        return stride
     if stride[-1] != 1 and shape[-1] != 1 or any(st == 0 and size > 1 for st, size in zip(stride, shape)):
         return None
     out, n = list(stride), 1
@@ -217,7 +218,7 @@ def _dense(shape, stride):
         if shape[i] > 1:
             out[i] = n
             n *= shape[i]
-    return shape, out
+    return out
 
 
 def apply_rotary(q, k=None, *, inv_freq, positions=None, layout: str = "interleaved", axes=None, scale: float = 1.0):
@@ -236,7 +237,23 @@ def apply_rotary(q, k=None, *, inv_freq, positions=None, layout: str = "interlea
     contiguous tensors: q' alone, or (q', k').
     """
     r = Rotary(inv_freq, positions, layout, axes, float(scale))
-    xs = (q,) if k is None else (q, k)
-    _check_inputs(xs)
-    out = RotaryFunction.apply(r, False, [None] * len(xs), *xs)
+    dtype, device = q.dtype, q.device
+    if dtype not in _DTYPES or k is not None and k.dtype not in _DTYPES:
+        raise TypeError("apply_rotary expects bf16, fp16 or fp32 tensors")
+    if k is not None and k.dtype != dtype:
+        raise TypeError("q and k must have one dtype")
+    if q.dim() != 4 or k is not None and k.dim() != 4:
+        raise ValueError("apply_rotary expects [B, H, N, d] tensors")
+    if device.type != "cuda" or k is not None and k.device != device:
+        raise ValueError("apply_rotary expects tensors on one CUDA device")
+    xs, wanted = (q,), q.requires_grad
+    if k is not None:
+        xs, wanted = (q, k), wanted or k.requires_grad
+        (B, _, N, d), other = q.shape, k.shape
+        if other[0] != B or other[2] != N or other[3] != d:
+            raise ValueError("q and k must agree in batch, length and head width")
+    if wanted and torch.is_grad_enabled():
+        out = RotaryFunction.apply(r, False, (None, None), *xs)
+    else:
+        out = tuple(_turned(r, False, (None, None), xs))
     return out[0] if k is None else out
