@@ -328,10 +328,10 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
  * spa2_sparse_attn_fwd (same o, bit for bit) and also writes q, k, v as 8-bit
  * checkpoints; nothing else needs to be kept for the backward pass (3.1 bytes per
  * element of q instead of the 10 of q, k, v, o and o_lo in bf16).
- * spa2_sparse_attn_bwd_ckpt reads the checkpoints, computes the attention again
- * from their values (LSE and D = rowsum(dO * O) in the workspace, O itself is not
- * stored) and writes dQ, dK, dV: the gradients of the attention at the kept
- * values, with the arithmetic of spa2_sparse_attn_bwd.
+ * spa2_sparse_attn_bwd_ckpt reads the checkpoints, finds the LSE of their values
+ * and D = rowsum(dO * O) = sum_j P_ij dP_ij again (O itself is not computed) and
+ * writes dQ, dK, dV: the gradients of the attention at the kept values, with the
+ * arithmetic of spa2_sparse_attn_bwd.
  * Keeping O and LSE instead of recomputing them is cheaper but not close: with q,
  * k, v rounded to 8 bits and O, LSE not, the rows of dS no longer sum to zero,
  * and sink keys of 8x norm amplify that to 12% of dQ (4% with recomputation).

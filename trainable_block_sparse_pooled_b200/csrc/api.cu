@@ -147,14 +147,12 @@ static BwdWs bwd_ws(void* ws, const Shape& s) {
   return w;
 }
 
-// the backward on 8-bit checkpoints: the backward's own workspace, then the kept
-// values of q, k, v and what the recomputed forward leaves
+// the backward on 8-bit checkpoints: the backward's own workspace, then the LSE that the dQ
+// pass finds and the kept values of k and v
 struct CkptWs {
   BwdWs b;
   float* lse;
-  void *q, *k, *v;  // [BH, N, d] bf16
-  void* v16;        // fp16 copy of v
-  void *o, *o_lo;
+  void *k, *v;  // [BH, N, d] bf16
   size_t bytes;
 };
 static CkptWs ckpt_ws(void* ws, const Shape& s) {
@@ -164,7 +162,7 @@ static CkptWs ckpt_ws(void* ws, const Shape& s) {
   size_t off = w.b.bytes;
   w.lse = reinterpret_cast<float*>(base + off);
   off += al256((size_t)s.BH * s.N * 4);
-  for (void** p : {&w.q, &w.k, &w.v, &w.v16, &w.o, &w.o_lo}) {
+  for (void** p : {&w.k, &w.v}) {
     *p = base + off;
     off += al256((size_t)s.BH * s.N * s.d * 2);
   }
@@ -455,7 +453,7 @@ spa2_status spa2_sparse_attn_bwd(const void* q, const void* k, const void* v, co
     cc = w.tiles.csc_cnt;
     ci = w.tiles.csc_idx;
   }
-  BwdArgs a{&tq, &tk, &tv, &tdo, &tq16, &tdq, q, k, o, o_lo, dout, v, lse, rc, ri, cc, ci, w.dvec, w.do16,
+  BwdArgs a{&tq, &tk, &tv, &tdo, &tq16, &tdq, q, k, o, o_lo, dout, v, const_cast<float*>(lse), rc, ri, cc, ci, w.dvec, w.do16,
             w.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
             scale * 1.4426950408889634f, w.status, w.status + 32, g_wait_limit_ns, s.tiled ? 1 : 0,
             w.col_order};
@@ -526,11 +524,9 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)d);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = grad_dtype == SPA2_DTYPE_F32;
-  CUtensorMap tq, tk, tv, tv16, to, tolo, tdo, tq16, tdq;
-  if (!make_map(&tq, w.q, s, 128) || !make_map(&tk, w.k, s, 64) || !make_map(&tv, w.v, s, 64) ||
-      !make_map(&tv16, w.v16, s, 64, true) || !make_map(&to, w.o, s, 128) || !make_map(&tolo, w.o_lo, s, 128) ||
-      !make_map(&tdo, w.b.do16, s, 128, true) || !make_map(&tq16, w.b.q16, s, 128, true) ||
-      !(f32 ? make_map_f32(&tdq, dq, s, 128) : make_map(&tdq, dq, s, 128)))
+  CUtensorMap tk, tv, tdo, tq16, tdq;
+  if (!make_map(&tk, w.k, s, 64) || !make_map(&tv, w.v, s, 64) || !make_map(&tdo, w.b.do16, s, 128, true) ||
+      !make_map(&tq16, w.b.q16, s, 128, true) || !(f32 ? make_map_f32(&tdq, dq, s, 128) : make_map(&tdq, dq, s, 128)))
     return SPA2_ERR_CUDA;
   int* status = w.b.status;
   SPA2_CUDA_TRY(cudaMemsetAsync(status, 0, 256, st));  // status word and the dK/dV column ticket
@@ -545,18 +541,15 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
     ci = t.csc_idx;
   }
   const long long rows = s.BH * s.N;
-  const spa2_pack8_tensor t[3] = {{w.q, q8->codes, q8->exps, rows, d},
+  const spa2_pack8_tensor t[3] = {{nullptr, q8->codes, q8->exps, rows, d},
                                   {w.k, k8->codes, k8->exps, rows, d},
                                   {w.v, v8->codes, v8->exps, rows, d}};
-  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, true, st));
-  SPA2_CUDA_TRY(launch_v_to_f16(w.v, w.v16, rows * d, status, st));
-  const float scale_log2 = scale * 1.4426950408889634f;
-  FwdArgs f{&tq, &tk, &tv16, &to, &tolo, 1, rc, ri, w.lse, (int)s.BH, s.N, s.TMt, s.TNt,
-            scale_log2, status, g_wait_limit_ns, s.tiled ? 1 : 0};
-  SPA2_CUDA_TRY(launch_fwd(f, d, st));
-  BwdArgs a{&tq, &tk, &tv, &tdo, &tq16, &tdq, w.q, w.k, w.o, w.o_lo, dout, w.v, w.lse, rc, ri, cc, ci, w.b.dvec,
-            w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale, scale_log2, status,
-            status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.b.col_order};
+  void* const f16[3] = {w.b.q16, nullptr, nullptr};
+  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, true, st, f16, status));
+  BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, w.k, nullptr, nullptr, dout, w.v, w.lse, rc, ri, cc, ci,
+            w.b.dvec, w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
+            scale * 1.4426950408889634f, status, status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.b.col_order,
+            q8->codes, q8->exps};
   SPA2_CUDA_TRY(launch_bwd(a, d, st));
   return SPA2_OK;
 }

@@ -477,6 +477,19 @@ SPA2_DEV int8_t pack8_code(float x, float scale) {
   const float y = fminf(fmaxf(x * scale, -1.984375f), 1.984375f);
   return (int8_t)(__float_as_uint(fmaf(y, 64.f, 12582912.f)) & 0xffu);
 }
+// the same of two values, as 16-bit integers, where scale64 = 64 * pack8_scale(E) is a
+// finite normal number (7 <= E <= 254): one product, clamped after the rounding
+SPA2_DEV uint32_t pack8_code2(float a, float b, float scale64) {
+  const uint32_t two = __byte_perm(__float_as_uint(fmaf(a, scale64, 12582912.f)),
+                                   __float_as_uint(fmaf(b, scale64, 12582912.f)), 0x5410);
+  return __vmins2(__vmaxs2(two, 0xff81ff81u), 0x007f007fu);
+}
+// the four codes of w as floats: a code plus 128 in the low bits of 2^23 is 2^23 + 128 + code
+SPA2_DEV void pack8_floats(uint32_t w, float (&f)[4]) {
+  w ^= 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | i)) - 8388736.f;
+}
 // 2^(E - 133), below E = 7 an fp32 subnormal; NaN for E = 255
 SPA2_DEV float pack8_step(uint32_t E) {
   return __uint_as_float(E >= 255u ? 0x7fffffffu : E >= 7u ? (E - 6u) << 23 : 1u << (16u + E));

@@ -92,13 +92,13 @@ struct BwdArgs {
   const CUtensorMap* tm_do;   // fp16 copy of dO, box {64, 128, 1}
   const CUtensorMap* tm_q16;  // fp16 copy of Q, box {64, 128, 1}
   const CUtensorMap* tm_dq;   // dQ output: fp32 box {32, 128, 1} or bf16 box {64, 128, 1}, 128-byte swizzle
-  const void* q;
+  const void* q;      // null with q8
   const void* k;
-  const void* o;
+  const void* o;      // null with q8
   const void* o_lo;   // may be null
   const void* dout;
   const void* v;
-  const float* lse;
+  float* lse;         // given, or (q8) written by the dQ pass
   const int* row_cnt;
   const int* row_idx;
   const int* col_cnt;
@@ -118,6 +118,10 @@ struct BwdArgs {
   unsigned long long wait_limit_ns;
   int tiled;          // list entries may carry tile exclusion bits
   int* col_order;     // [BH * Tn]: the dK/dV pass's columns, head by head, long columns first (pre-pass)
+  // on 8-bit checkpoints (otherwise null): Q's codes and exponents; q16 is already there, k and v
+  // are the kept values
+  const int8_t* q8;
+  const uint8_t* qe;
 };
 cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s);
 

@@ -20,8 +20,8 @@ namespace spa2 {
 namespace {
 
 struct Pack8Args {
-  spa2_pack8_tensor t[SPA2_PACK8_MAX];
-  uint32_t* f16[SPA2_PACK8_MAX];  // fp16 copy of the tensor (packing) or of its values, or null
+  spa2_pack8_tensor t[SPA2_PACK8_MAX];  // unpacking with f16, x may be null
+  uint32_t* f16[SPA2_PACK8_MAX];        // fp16 copy of the tensor (packing) or of its values, or null
   int* status;                    // where |x| > 65504 is reported; needed for a copy
 };
 
@@ -84,6 +84,18 @@ SPA2_DEV uint32_t chunk_exponent(const Chunk<T>& x) {
   }
 }
 
+// fp16 copy of a chunk; below 2^16 (E <= 142) only fp32 inputs could exceed 65504 by rounding,
+// and copies are made of bf16 tensors and of codes (7 bits): no element needs a look
+SPA2_DEV void store_f16(uint32_t* to, const float (&f)[CHUNK], uint32_t E, bool& bad) {
+  uint4 w;
+  if (E <= 142u)
+    w = make_uint4(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7]));
+  else
+    w = make_uint4(pack_f16_clamped(f[0], f[1], bad), pack_f16_clamped(f[2], f[3], bad),
+                   pack_f16_clamped(f[4], f[5], bad), pack_f16_clamped(f[6], f[7], bad));
+  *reinterpret_cast<uint4*>(to) = w;
+}
+
 }  // namespace
 
 template <typename T, bool FLAT>
@@ -107,23 +119,24 @@ __global__ void __launch_bounds__(THREADS) pack8_kernel(const __grid_constant__ 
     E = max(E, __shfl_xor_sync(0xffffffffu, E, 1));
     E = max(E, __shfl_xor_sync(0xffffffffu, E, 2));
     if (!here[u]) continue;
-    const float scale = pack8_scale(E);
-    union {
-      int8_t c[CHUNK];
-      uint2 w;
-    } code;
     float f[CHUNK];
 #pragma unroll
-    for (int i = 0; i < CHUNK; ++i) {
-      f[i] = static_cast<float>(x[u].e[i]);
-      code.c[i] = pack8_code(f[i], scale);
+    for (int i = 0; i < CHUNK; ++i) f[i] = static_cast<float>(x[u].e[i]);
+    uint32_t c[4];  // codes as 16-bit integers
+    if (E - 7u < 248u) {
+      const float scale64 = __uint_as_float((260u - E) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = pack8_code2(f[2 * i], f[2 * i + 1], scale64);
+    } else {  // magnitudes below 2^-120, or a group whose codes do not matter
+      const float scale = pack8_scale(E);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c[i] = __byte_perm((int)pack8_code(f[2 * i], scale), (int)pack8_code(f[2 * i + 1], scale), 0x5410);
     }
-    *reinterpret_cast<uint2*>(t.codes + e[u]) = code.w;
+    *reinterpret_cast<uint2*>(t.codes + e[u]) =
+        make_uint2(__byte_perm(c[0], c[1], 0x6420), __byte_perm(c[2], c[3], 0x6420));
     if (threadIdx.x % PER_GROUP == 0) t.exps[group[u]] = (uint8_t)E;
-    if (f16)
-      *reinterpret_cast<uint4*>(f16 + e[u] / 2) =
-          make_uint4(pack_f16_clamped(f[0], f[1], bad), pack_f16_clamped(f[2], f[3], bad),
-                     pack_f16_clamped(f[4], f[5], bad), pack_f16_clamped(f[6], f[7], bad));
+    if (f16) store_f16(f16 + e[u] / 2, f, E, bad);
   }
   if (bad) report(a.status, SPA2_ERR_RANGE);
 }
@@ -149,19 +162,17 @@ __global__ void __launch_bounds__(THREADS) unpack8_kernel(const __grid_constant_
   for (int u = 0; u < UNROLL; ++u) {
     if (!here[u]) continue;
     const float step = pack8_step(E[u]);
-    float f[CHUNK];
+    float lo[4], hi[4], f[CHUNK];
+    pack8_floats(code[u].x, lo);
+    pack8_floats(code[u].y, hi);
     Chunk<T> x;
 #pragma unroll
     for (int i = 0; i < CHUNK; ++i) {
-      const uint32_t w = i < 4 ? code[u].x : code[u].y;
-      f[i] = static_cast<float>((int8_t)(w >> (8 * (i & 3)))) * step;
+      f[i] = (i < 4 ? lo[i & 3] : hi[i & 3]) * step;
       x.e[i] = static_cast<T>(f[i]);
     }
-    *reinterpret_cast<Chunk<T>*>(static_cast<T*>(t.x) + e[u]) = x;
-    if (f16)
-      *reinterpret_cast<uint4*>(f16 + e[u] / 2) =
-          make_uint4(pack_f16_clamped(f[0], f[1], bad), pack_f16_clamped(f[2], f[3], bad),
-                     pack_f16_clamped(f[4], f[5], bad), pack_f16_clamped(f[6], f[7], bad));
+    if (t.x) *reinterpret_cast<Chunk<T>*>(static_cast<T*>(t.x) + e[u]) = x;
+    if (f16) store_f16(f16 + e[u] / 2, f, E[u], bad);
   }
   if (bad) report(a.status, SPA2_ERR_RANGE);
 }

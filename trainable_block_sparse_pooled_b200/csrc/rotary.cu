@@ -93,38 +93,43 @@ __global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ Rot
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) cs[i] = cos_sin(a, b, n, u * PAIRS + i);
   }
-  const int h1 = min(a.heads, (int)(blockIdx.y + 1) * a.per_block);
-  for (int h = blockIdx.y * a.per_block; h < h1; h += HB) {
-    VT x[HB], z[HB];
-    T* y[HB];
+  const int first = blockIdx.y * a.per_block, last = min(a.heads, first + a.per_block);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {  // this block's heads of the first tensor, then of the second
+    const int lo = which ? max(first - a.heads0, 0) : first;
+    const int hi = which ? last - a.heads0 : min(last, a.heads0);
+    const RotaryTensor& t = a.t[which];
+    const T* from = static_cast<const T*>(t.x) + b * t.xs[0] + lo * t.xs[1] + n * t.xs[2];
+    T* to = static_cast<T*>(t.y) + b * t.ys[0] + lo * t.ys[1] + n * t.ys[2];
+#pragma unroll 1
+    for (int h = lo; h < hi; h += HB) {
+      VT x[HB], z[HB];
 #pragma unroll
-    for (int i = 0; i < HB; ++i) {
-      if (h + i < h1) {
-        const bool second = h + i >= a.heads0;
-        const RotaryTensor& t = a.t[second];
-        const int hh = h + i - (second ? a.heads0 : 0);
-        const T* from = static_cast<const T*>(t.x) + b * t.xs[0] + hh * t.xs[1] + n * t.xs[2];
-        y[i] = static_cast<T*>(t.y) + b * t.ys[0] + hh * t.ys[1] + n * t.ys[2];
-        x[i] = *reinterpret_cast<const VT*>(from + e0);
-        if (SPLIT && !copy) z[i] = *reinterpret_cast<const VT*>(from + e1);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < HB; ++i) {
-      if (h + i < h1) {
-        if (!copy) {
-#pragma unroll
-          for (int p = 0; p < PAIRS; ++p) {
-            T& s = x[i].e[SPLIT ? p : 2 * p];
-            T& t = SPLIT ? z[i].e[p] : x[i].e[2 * p + 1];
-            float v, w;
-            turn(static_cast<float>(s), static_cast<float>(t), cs[p], v, w);
-            s = from_f32<T>(v);
-            t = from_f32<T>(w);
-          }
-          if (SPLIT) *reinterpret_cast<VT*>(y[i] + e1) = z[i];
+      for (int i = 0; i < HB; ++i) {
+        if (h + i < hi) {
+          x[i] = *reinterpret_cast<const VT*>(from + e0);
+          if (SPLIT && !copy) z[i] = *reinterpret_cast<const VT*>(from + e1);
+          from += t.xs[1];
         }
-        *reinterpret_cast<VT*>(y[i] + e0) = x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < HB; ++i) {
+        if (h + i < hi) {
+          if (!copy) {
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) {
+              T& s = x[i].e[SPLIT ? p : 2 * p];
+              T& w = SPLIT ? z[i].e[p] : x[i].e[2 * p + 1];
+              float ox, oy;
+              turn(static_cast<float>(s), static_cast<float>(w), cs[p], ox, oy);
+              s = from_f32<T>(ox);
+              w = from_f32<T>(oy);
+            }
+            if (SPLIT) *reinterpret_cast<VT*>(to + e1) = z[i];
+          }
+          *reinterpret_cast<VT*>(to + e0) = x[i];
+          to += t.ys[1];
+        }
       }
     }
   }
