@@ -360,6 +360,13 @@ SPA2_API spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, cons
 SPA2_API spa2_status spa2_stream_status(void* ws, spa2_stream_t stream);
 
 /*
+ * Queues a copy of the status word at the start of `ws` to `host` (pinned memory),
+ * behind what `stream` holds, without waiting for it. SPA2_OK, or the error of the
+ * copy itself.
+ */
+SPA2_API spa2_status spa2_status_fetch(const void* ws, int32_t* host, spa2_stream_t stream);
+
+/*
  * Fault-path testing. Sets the time limit, in nanoseconds, of every bounded
  * device-side wait launched afterwards by this process (default 2e9 = 2 s;
  * limit <= 0 restores the default). Returns SPA2_OK.

@@ -44,54 +44,52 @@ _cache: dict = {}
 
 
 class _StatusWatch:
-    """Stream-ordered, non-blocking copies of one Spa2's status words."""
+    """Stream-ordered, non-blocking copies of one Spa2's status words into pinned memory. A
+    slot holds PENDING until its copy lands, so a look at it needs no event."""
 
-    SLOTS = 16
+    SLOTS, PENDING = 16, -1
 
     def __init__(self, spa: b.Spa2):
         self.spa = spa
         self.host = torch.zeros(self.SLOTS, 3, dtype=torch.int32).pin_memory()
         self.codes = self.host.numpy()
-        self.places = [[self.host[i, j:j + 1] for j in range(3)] for i in range(self.SLOTS)]
-        self.words: dict = {}              # op -> its status word on the device
-        self.events: list = [None] * self.SLOTS
-        self.pending: deque = deque()      # (slot, event, ops) in launch order
+        self.pending: deque = deque()      # (slot, ops) in launch order
         self.next = 0
 
     def after(self, ops):
         """Queue a copy of the status words of `ops` behind the work just launched."""
         if len(self.pending) == self.SLOTS:
-            self._finish(self.pending.popleft(), wait=True)
+            self._finish(wait=True)
         slot = self.next
         self.next = (self.next + 1) % self.SLOTS
-        for place, op in zip(self.places[slot], ops):
-            word = self.words.get(op)
-            if word is None:
-                word = self.words[op] = self.spa.ws[op][:4].view(torch.int32)
-            place.copy_(word, non_blocking=True)
-        ev = self.events[slot]
-        if ev is None:
-            ev = self.events[slot] = torch.cuda.Event()
-        ev.record()
-        self.pending.append((slot, ev, tuple(ops)))
+        at, stream = self.host.data_ptr() + 12 * slot, b._stream(torch)
+        for col, op in enumerate(ops):
+            self.codes[slot, col] = self.PENDING
+            b._check(b.spa2_status_fetch(self.spa.ws[op].data_ptr(), at + 4 * col, stream), "spa2_status_fetch")
+        self.pending.append((slot, ops))
 
     def poll(self):
         """Raise the first error among copies that have landed (never waits)."""
-        while self.pending and self.pending[0][1].query():
-            self._finish(self.pending.popleft(), wait=False)
+        while self.pending and self._landed():
+            self._finish(wait=False)
 
     def drain(self):
         """Wait for every pending copy, then raise the first error among them."""
         while self.pending:
-            self._finish(self.pending.popleft(), wait=True)
+            self._finish(wait=True)
 
-    def _finish(self, item, wait):
-        slot, ev, ops = item
-        if wait:
-            ev.synchronize()
+    def _landed(self):
+        slot, ops = self.pending[0]
+        return self.codes[slot, len(ops) - 1] != self.PENDING   # the copies of a slot land in order
+
+    def _finish(self, wait):
+        if wait and not self._landed():
+            torch.cuda.synchronize(self.spa.device)
+        slot, ops = self.pending.popleft()
         for col, op in enumerate(ops):
             code = int(self.codes[slot, col])
             if code != b.OK:
+                torch.cuda.synchronize(self.spa.device)  # no copy lands in a slot that is used again
                 self.pending.clear()
                 raise b.Spa2Error(code, f"device status of sparse_attention (op {op})")
 
@@ -185,7 +183,7 @@ class CheckpointedAttentionFunction(torch.autograd.Function):
         s = _spa(*q.shape, q.device, bq, bkv)
         o, kept = s.fwd_ckpt(q, k, v, mask, scale)
         s.watch.after((b.OP_FWD,))
-        ctx.save_for_backward(*[p.data for p in kept])
+        ctx.save_for_backward(kept[0].base)
         ctx.mask, ctx.scale, ctx.blocks = mask, scale, (bq, bkv)
         return o
 
@@ -194,7 +192,7 @@ class CheckpointedAttentionFunction(torch.autograd.Function):
     def backward(ctx, do):
         shape, dtype = do.shape, do.dtype
         s = _spa(*shape, do.device, *ctx.blocks)
-        kept = [Packed(data, shape, dtype) for data in ctx.saved_tensors]
+        kept = Packed.several_in(ctx.saved_tensors[0], shape, dtype, 3)
         grads = s.bwd_ckpt(kept, do.contiguous(), ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
         s.watch.after((b.OP_BWD_CKPT,))
         return (*grads, None, None, None, None)

@@ -117,6 +117,7 @@ _SIGS = {
                                   + [ctypes.c_int] * 6 + [ctypes.POINTER(spa2_mask), ctypes.c_float]
                                   + [ctypes.c_void_p] * 3 + [ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
                                                              ctypes.c_void_p]),
+    "spa2_status_fetch": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "spa2_stream_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "spa2_debug_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_longlong]),
     "spa2_debug_timeout_probe": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
@@ -196,6 +197,7 @@ def spa2_sparse_attn_bwd(q, k, v, o, o_lo, lse, dout, B, H, N, d, bq, bkv, mask:
 
 # The structures' bytes, which struct packs several times as fast as ctypes fills fields
 # (a call of a few tokens is mostly the host's time).
+_POINTER = struct.Struct("@P")
 _ROTARY_SPEC = struct.Struct("@Pi3q5iP2if0q")
 _ROTARY_TENSOR = "PPi6q"
 _PACK8_TENSOR = "PPPqq"
@@ -209,6 +211,16 @@ def rotary_spec(positions, position_bytes, position_stride, pairs, inv_freq, rot
     """A spa2_rotary_spec as bytes: pointers (or None), strides (batch, axis, token), the pairs of each axis."""
     return _ROTARY_SPEC.pack(positions or 0, position_bytes, *position_stride, len(pairs),
                              *pairs, *(0,) * (ROTARY_MAX_AXES - len(pairs)), inv_freq, rotary_dim, layout, scale)
+
+
+_ROTARY_INV_FREQ = spa2_rotary_spec.inv_freq.offset
+
+
+def rotary_spec_points(spec: bytes, inv_freq, positions) -> bool:
+    """Whether a rotary_spec holds the addresses of these tensors."""
+    at = 0 if positions is None else positions.data_ptr()
+    return _POINTER.unpack_from(spec, 0)[0] == at and \
+        _POINTER.unpack_from(spec, _ROTARY_INV_FREQ)[0] == inv_freq.data_ptr()
 
 
 def spa2_rotary(tensors, B, N, d, dtype, spec: spa2_rotary_spec, inverse, stream) -> int:
@@ -236,6 +248,10 @@ def spa2_sparse_attn_bwd_ckpt(q8: spa2_pack8_tensor, k8: spa2_pack8_tensor, v8: 
     return lib().spa2_sparse_attn_bwd_ckpt(ctypes.byref(q8), ctypes.byref(k8), ctypes.byref(v8), dout, B, H, N, d, bq,
                                            bkv, ctypes.byref(mask), scale, dq, dk, dv, grad_dtype, ws, ws_bytes,
                                            stream)
+
+
+def spa2_status_fetch(ws, host, stream) -> int:
+    return lib().spa2_status_fetch(ws, host, stream)
 
 
 def spa2_stream_status(ws, stream) -> int:
@@ -394,7 +410,7 @@ class Spa2:
         from .checkpoint import Packed
         t = self.torch
         o = t.empty_like(q)
-        kept = tuple(Packed.empty_like(x) for x in (q, k, v))
+        kept = Packed.several_like(q, 3)
         cm = mask.c()
         ws = self.ws[OP_FWD]
         _check(spa2_sparse_attn_fwd_ckpt(q.data_ptr(), k.data_ptr(), v.data_ptr(), self.B, self.H, self.N, self.d,

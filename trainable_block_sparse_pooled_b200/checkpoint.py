@@ -27,12 +27,12 @@ _DTYPES = {torch.bfloat16: b.DTYPE_BF16, torch.float32: b.DTYPE_F32, torch.float
 
 
 class Packed:
-    """One tensor as 8-bit codes and exponent bytes, both in one device buffer."""
+    """One tensor as 8-bit codes and exponent bytes, both in one device buffer (or a part of it)."""
 
-    __slots__ = ("data", "shape", "dtype")
+    __slots__ = ("base", "offset", "shape", "dtype")
 
-    def __init__(self, data: torch.Tensor, shape, dtype: torch.dtype):
-        self.data, self.shape, self.dtype = data, torch.Size(shape), dtype
+    def __init__(self, base: torch.Tensor, shape, dtype: torch.dtype, offset: int = 0):
+        self.base, self.offset, self.shape, self.dtype = base, offset, shape, dtype
 
     @staticmethod
     def _sizes(shape):
@@ -45,6 +45,22 @@ class Packed:
         shape = x.shape
         _, at, groups = cls._sizes(shape)
         return cls(torch.empty(at + groups, dtype=torch.uint8, device=x.device), shape, x.dtype)
+
+    @classmethod
+    def several_like(cls, x: torch.Tensor, n: int) -> tuple:
+        """n checkpoints of tensors like x in one buffer."""
+        _, at, groups = cls._sizes(x.shape)
+        size = n * ((at + groups + 15) & ~15)
+        return cls.several_in(torch.empty(size, dtype=torch.uint8, device=x.device), x.shape, x.dtype, n)
+
+    @classmethod
+    def several_in(cls, base, shape, dtype, n) -> tuple:
+        return tuple([cls(base, shape, dtype, i * (base.shape[0] // n)) for i in range(n)])
+
+    @property
+    def data(self) -> torch.Tensor:
+        """The bytes: codes, padded to a multiple of 16, then exponents."""
+        return self.base[self.offset:self.offset + self.nbytes]
 
     @property
     def codes(self) -> torch.Tensor:
@@ -59,12 +75,13 @@ class Packed:
 
     @property
     def nbytes(self) -> int:
-        return self.data.numel()
+        _, at, groups = self._sizes(self.shape)
+        return at + groups
 
     def fields(self, x: torch.Tensor | None = None) -> tuple:
         """The fields of a spa2_pack8_tensor of this checkpoint and x (contiguous, of its shape)."""
         n, at, _ = self._sizes(self.shape)
-        p, d = self.data.data_ptr(), self.shape[-1]
+        p, d = self.base.data_ptr() + self.offset, self.shape[-1]
         return 0 if x is None else x.data_ptr(), p, p + at, n // d, d
 
     def c(self, x: torch.Tensor | None = None) -> b.spa2_pack8_tensor:
@@ -108,12 +125,12 @@ def unpack8(*packed: Packed) -> tuple[torch.Tensor, ...]:
     """The kept values of each checkpoint, contiguous, in its tensor's shape and dtype."""
     if not packed:
         raise ValueError("unpack8 expects at least one checkpoint")
-    dtype, device = packed[0].dtype, packed[0].data.device
+    dtype, device = packed[0].dtype, packed[0].base.device
     for p in packed:
         if p.dtype != dtype:
             raise TypeError("unpack8 expects checkpoints of tensors of one dtype")
     for p in packed:
-        if p.data.device != device or device.type != "cuda":
+        if p.base.device != device or device.type != "cuda":
             raise ValueError("unpack8 expects checkpoints on one CUDA device")
     items = [(p, torch.empty(p.shape, dtype=dtype, device=device)) for p in packed]
     _launch(b.lib().spa2_unpack8, items, dtype, device, "spa2_unpack8")

@@ -554,6 +554,13 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
   return SPA2_OK;
 }
 
+spa2_status spa2_status_fetch(const void* ws, int32_t* host, spa2_stream_t stream) {
+  if (!ws) return SPA2_ERR_WORKSPACE;
+  if (!host || !aligned(host, 4)) return SPA2_ERR_INVALID_ARG;
+  SPA2_CUDA_TRY(cudaMemcpyAsync(host, ws, 4, cudaMemcpyDeviceToHost, reinterpret_cast<cudaStream_t>(stream)));
+  return SPA2_OK;
+}
+
 spa2_status spa2_stream_status(void* ws, spa2_stream_t stream) {
   if (!ws) return SPA2_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

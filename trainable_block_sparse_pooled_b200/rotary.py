@@ -147,33 +147,28 @@ def _spec(r: Rotary, B: int, N: int, d: int, device) -> tuple:
     return b.rotary_spec(at, size, stride, axes, f.data_ptr(), 2 * pairs, layout, r.scale), f
 
 
-def _turn(xs, outs, r: Rotary, inverse: bool):
-    """outs[i] <- xs[i] turned; every tensor [B, H, N, d] with a contiguous last dimension."""
+def _turned(spec, inverse: bool, strides, xs):
+    """xs turned by the spa2_rotary_spec `spec`, each in strides of its own or (None) contiguous."""
     x = xs[0]
-    B, _, N, d = x.shape
-    device = x.device
-    spec, keep = _spec(r, B, N, d, device)  # keep: what the call reads on the current stream
-    fields = []
-    for x, y in zip(xs, outs):
-        heads = x.shape[1]
-        if B and heads and N:
-            fields += x.data_ptr(), y.data_ptr(), heads, *x.stride()[:3], *y.stride()[:3]
+    (B, _, N, d), dtype, device = x.shape, x.dtype, x.device
+    fields, outs, keep = [], [], []
+    for x, st in zip(xs, strides):
+        shape = x.shape
+        if x.stride(3) != 1 and d != 1:
+            x = x.contiguous()
+            keep.append(x)
+        y = torch.empty(shape, dtype=dtype, device=device) if st is None else \
+            torch.empty_strided(shape, st, dtype=dtype, device=device)
+        outs.append(y)
+        if B and shape[1] and N:
+            fields += x.data_ptr(), y.data_ptr(), shape[1], *x.stride()[:3], *y.stride()[:3]
     n = len(fields) // 9
-    if n == 0:
-        return
-    with b.on_device(device):
-        rc = b.lib().spa2_rotary(b.ROTARY_TENSORS[n].pack(*fields), n, B, N, d, _DTYPES[x.dtype], spec, inverse,
-                                 b._stream(torch))
-    if rc != b.OK:
-        raise b.Spa2Error(rc, "spa2_rotary")
-
-
-def _turned(r: Rotary, inverse: bool, strides, xs):
-    """xs turned, each in strides of its own or (None) contiguous."""
-    xs = [x if x.stride(-1) == 1 or x.shape[-1] == 1 else x.contiguous() for x in xs]
-    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) if st is None else
-            torch.empty_strided(x.shape, st, dtype=x.dtype, device=x.device) for x, st in zip(xs, strides)]
-    _turn(xs, outs, r, inverse)
+    if n:
+        with b.on_device(device):
+            rc = b.lib().spa2_rotary(b.ROTARY_TENSORS[n].pack(*fields), n, B, N, d, _DTYPES[dtype], spec, inverse,
+                                     b._stream(torch))
+        if rc != b.OK:
+            raise b.Spa2Error(rc, "spa2_rotary")
     return outs
 
 
@@ -182,11 +177,13 @@ class RotaryFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, r: Rotary, inverse: bool, strides, *xs):
+        B, _, N, d = xs[0].shape
+        spec, f = _spec(r, B, N, d, xs[0].device)
         ctx.save_for_backward(r.inv_freq, r.positions)  # so that a change in between is noticed
-        ctx.spec, ctx.inverse = (r.layout, r.axes, r.scale), inverse
+        ctx.r, ctx.spec, ctx.inverse = (r.layout, r.axes, r.scale), spec, inverse
         ctx.strides = [_dense(x) for x in xs]
         ctx.set_materialize_grads(False)
-        return tuple(_turned(r, inverse, strides, xs))
+        return tuple(_turned(spec, inverse, strides, xs))
 
     @staticmethod
     def backward(ctx, *grads):
@@ -194,12 +191,16 @@ class RotaryFunction(torch.autograd.Function):
         at = [i for i, g in enumerate(grads) if g is not None and wanted[3 + i]]
         out = [None] * len(grads)
         if at:
-            r = Rotary(*ctx.saved_tensors, *ctx.spec)
+            r = Rotary(*ctx.saved_tensors, *ctx.r)
             strides, xs = [ctx.strides[i] for i in at], [grads[i] for i in at]
             if torch.is_grad_enabled():  # the gradient will be differentiated itself
                 turned = RotaryFunction.apply(r, not ctx.inverse, strides, *xs)
             else:
-                turned = _turned(r, not ctx.inverse, strides, xs)
+                B, _, N, d = xs[0].shape
+                spec, f = ctx.spec, None
+                if not b.rotary_spec_points(spec, r.inv_freq, r.positions):  # copies of the saved tensors
+                    spec, f = _spec(r, B, N, d, xs[0].device)
+                turned = _turned(spec, not ctx.inverse, strides, xs)
             for i, g in zip(at, turned):
                 out[i] = g
         return (None, None, None, *out)
@@ -255,5 +256,7 @@ def apply_rotary(q, k=None, *, inv_freq, positions=None, layout: str = "interlea
     if wanted and torch.is_grad_enabled():
         out = RotaryFunction.apply(r, False, (None, None), *xs)
     else:
-        out = tuple(_turned(r, False, (None, None), xs))
+        B, _, N, d = q.shape
+        spec, f = _spec(r, B, N, d, device)
+        out = tuple(_turned(spec, False, (None, None), xs))
     return out[0] if k is None else out
