@@ -22,7 +22,9 @@ namespace {
 struct Pack8Args {
   spa2_pack8_tensor t[SPA2_PACK8_MAX];  // unpacking with f16, x may be null
   uint32_t* f16[SPA2_PACK8_MAX];        // fp16 copy of the tensor (packing) or of its values, or null
-  int* status;                    // where |x| > 65504 is reported; needed for a copy
+  int* status;                          // where |x| > 65504 is reported; needed for a copy
+  uint32_t per_row[SPA2_PACK8_MAX];     // chunk places of a row, and x / per_row = x * div_mul >> (32 + div_shift)
+  uint32_t div_mul[SPA2_PACK8_MAX], div_shift[SPA2_PACK8_MAX];  // for x < 2^31
 };
 
 constexpr int CHUNK = 8, PER_GROUP = 4, UNROLL = 4, THREADS = 256;
@@ -37,13 +39,15 @@ struct alignas(16) Chunk {
 // last group of a row may hold places without a chunk. One thread's places of a block:
 template <bool FLAT>
 struct Places {
-  uint32_t per_row, first;
+  uint32_t per_row, mul, shift, first;
   long long row0, base;
 
-  SPA2_DEV Places(const spa2_pack8_tensor& t) {
+  SPA2_DEV Places(const Pack8Args& a) {
     base = (long long)blockIdx.x * PLACES;
     if (!FLAT) {
-      per_row = (uint32_t)((t.d + 31) / 32 * PER_GROUP);
+      per_row = a.per_row[blockIdx.y];
+      mul = a.div_mul[blockIdx.y];
+      shift = a.div_shift[blockIdx.y];
       row0 = base / per_row;
       first = (uint32_t)(base - row0 * per_row);
     }
@@ -55,7 +59,7 @@ struct Places {
       group = (base + c) / PER_GROUP;
       return e < t.rows * t.d;
     }
-    const uint32_t p = first + c, r = p / per_row, col = p - r * per_row;
+    const uint32_t p = first + c, r = __umulhi(p, mul) >> shift, col = p - r * per_row;
     const long long row = row0 + r;
     e = row * t.d + (long long)col * CHUNK;
     group = row * (per_row / PER_GROUP) + col / PER_GROUP;
@@ -99,10 +103,10 @@ SPA2_DEV void store_f16(uint32_t* to, const float (&f)[CHUNK], uint32_t E, bool&
 }  // namespace
 
 template <typename T, bool FLAT>
-__global__ void __launch_bounds__(THREADS) pack8_kernel(const __grid_constant__ Pack8Args a) {
+__global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) pack8_kernel(const __grid_constant__ Pack8Args a) {
   pdl_trigger();
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
-  const Places<FLAT> places(t);
+  const Places<FLAT> places(a);
   uint32_t* f16 = a.f16[blockIdx.y];
   long long e[UNROLL], group[UNROLL];
   bool here[UNROLL], bad = false;
@@ -142,9 +146,9 @@ __global__ void __launch_bounds__(THREADS) pack8_kernel(const __grid_constant__ 
 }
 
 template <typename T, bool FLAT>
-__global__ void __launch_bounds__(THREADS) unpack8_kernel(const __grid_constant__ Pack8Args a) {
+__global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) unpack8_kernel(const __grid_constant__ Pack8Args a) {
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
-  const Places<FLAT> places(t);
+  const Places<FLAT> places(a);
   uint32_t* f16 = a.f16[blockIdx.y];
   long long e[UNROLL], group;
   bool here[UNROLL], bad = false;
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(THREADS) unpack8_single_kernel(const __grid_co
 }
 
 template <typename T>
-static cudaError_t launch_pack8_t(const Pack8Args& a, int n, bool unpack, cudaStream_t s) {
+static cudaError_t launch_pack8_t(Pack8Args& a, int n, bool unpack, cudaStream_t s) {
   long long groups = 0;
   bool chunks = true, flat = true;
   for (int i = 0; i < n; ++i) {
@@ -213,6 +217,15 @@ static cudaError_t launch_pack8_t(const Pack8Args& a, int n, bool unpack, cudaSt
     chunks &= t.d % CHUNK == 0 && t.d < (1LL << 31) && reinterpret_cast<uintptr_t>(t.x) % 16 == 0 &&
               reinterpret_cast<uintptr_t>(t.codes) % CHUNK == 0;
     flat &= t.d % SPA2_PACK8_GROUP == 0;
+    // x / p = x * ceil(2^(31 + l) / p) >> (31 + l) for x < 2^31, with 2^l >= p the next power of two
+    const uint64_t p = (uint64_t)((t.d + 31) / 32 * PER_GROUP);
+    if (chunks) {
+      uint32_t l = 0;
+      while ((1ull << l) < p) ++l;
+      a.per_row[i] = (uint32_t)p;
+      a.div_mul[i] = (uint32_t)(((1ull << (31 + l)) + p - 1) / p);
+      a.div_shift[i] = l - 1;
+    }
   }
   if (groups == 0) return cudaSuccess;
   KernelTimer kt(unpack ? KID_UNPACK8 : KID_PACK8, s);

@@ -76,7 +76,7 @@ SPA2_DEV void turn(float x, float y, float2 cs, float& ox, float& oy) {
 }  // namespace
 
 template <typename T, int V, bool SPLIT>
-__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(256, 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int PAIRS = SPLIT ? V : V / 2;  // pairs of a unit
   constexpr int HB = SPLIT ? 2 : 4;         // heads in flight: 4 loads
   using VT = Vec<T, V>;
