@@ -19,7 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libspa2.so")
 SOURCES = ["api.cu", "mask.cu", "attn_fwd.cu", "attn_bwd.cu", "noalloc.cu", "timing.cu", "tiles.cu",
-           "rotary.cu", "pack8.cu"]
+           "rotary.cu", "pack8.cu", "attn_bwd_ckpt.cu"]
 HEADERS = ["common.cuh", "kernels.h"]
 
 NVCC_FLAGS = [

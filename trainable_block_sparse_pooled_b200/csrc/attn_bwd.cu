@@ -589,17 +589,8 @@ namespace {
 constexpr int DQ_THREADS = 320;  // dS x 8 warps, TMA, MMA
 constexpr int DQ_KS = 6;         // K / V ring slots
 
-// what the first pass of the checkpointed form leaves: for each half of the kv columns the
-// rows' maximum, sum of exponentials and sum of those times dP
-template <bool CKPT>
-struct DqStats {};
-template <>
-struct DqStats<true> {
-  float part[2][3][128];
-};
-
-template <int D, bool CKPT>
-struct DqSmem : DqStats<CKPT> {
+template <int D>
+struct DqSmem {
   static constexpr int CH = D / 64;
   alignas(1024) uint8_t k[DQ_KS][CH][64 * 128];    // K_j bf16
   alignas(1024) uint8_t v[DQ_KS][CH][64 * 128];    // V_j bf16
@@ -621,24 +612,14 @@ struct DqSmem : DqStats<CKPT> {
 // 128 bytes per cycle the tensor core can read from shared memory).
 // TMEM columns: S[b] 64b .. 64b+63 (dS hi/lo of kv columns 32h .. 32h+31 go to
 // 64b+32h .. +15 / +16 .. +31), dP[b] 128+64b, dQ 256 .. 256+d, Q 384, dO 448.
-//
-// CKPT (the backward on 8-bit checkpoints): LSE and D are not given but found first, by a
-// pass over the same tiles that forms S and dP and nothing else,
-//   l = sum_j 2^(x_ij - m),  w = sum_j 2^(x_ij - m) dP_ij,  LSE = m + log2 l,  D = w / l
-// (D = sum_j P_ij dP_ij is rowsum(dO * O)), kept in fp32 with a running maximum m; it writes
-// both for the dK/dV pass, which then follows. So the attention's output is not computed
-// again: no P V product, no store and no load of O. Two products a tile instead of the
-// forward's two and its P in between. Q_i is decoded from its codes on the way into TMEM.
-template <int D, bool TILED, bool CKPT>
+template <int D, bool TILED>
 __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                                const __grid_constant__ CUtensorMap tm_v,
                                                                const __grid_constant__ CUtensorMap tm_dq,
                                                                const __nv_bfloat16* __restrict__ qg,
-                                                               const int8_t* __restrict__ q8,
-                                                               const uint8_t* __restrict__ qe,
                                                                const __nv_bfloat16* __restrict__ dout,
-                                                               float* __restrict__ lse,
-                                                               float* __restrict__ dvec,
+                                                               const float* __restrict__ lse,
+                                                               const float* __restrict__ dvec,
                                                                const int* __restrict__ row_cnt,
                                                                const int* __restrict__ row_idx,
                                                                int grad_f32, int N, int Tm, int Tn, float scale,
@@ -653,7 +634,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
   constexpr float LOG2E = 1.4426950408889634f;
 
   extern __shared__ uint8_t smem_raw[];
-  DqSmem<D, CKPT>& sm = *reinterpret_cast<DqSmem<D, CKPT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DqSmem<D>& sm = *reinterpret_cast<DqSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);  // warp-uniform
   const uint32_t lane = lane_id();
@@ -694,8 +675,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
     n = 0;
   }
   const int* kv_list = row_idx + rowid * Tn;
-  const int t_dq = CKPT ? n : 0;  // the ring's tile at which the pass that forms dQ begins
-  const int t_end = t_dq + n;
   int epi_ok = 1;  // a dS thread clears it when its part of the dQ tile was not staged
 
   if (warp == 8) {
@@ -704,10 +683,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       int issued = 0;
-      for (int t = 0; t < t_end; ++t) {
+      for (int t = 0; t < n; ++t) {
         const int slot = t % DQ_KS;
         if (t >= DQ_KS && !wait_bar(&sm.kv_empty[slot], ((t / DQ_KS) - 1) & 1, wc)) break;
-        const int j = kv_list[t < n ? t : t - n] & TILE_ID_MASK;
+        const int j = kv_list[t] & TILE_ID_MASK;
         if (j >= Tn) {
           report(status, SPA2_ERR_DEVICE_BOUNDS);
           sm.abort_flag = 1;
@@ -727,12 +706,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
     // ---------------- MMA issuer: S(t), dP(t), then dQ += dS(t-1) K(t-1), all TS ----------------
     if (n > 0) {  // all 32 lanes; elect.sync picks the issuing lane
       if (wait_bar_all(&sm.qd_ready, 0, wc)) {
-        for (int t = 0; t <= t_end; ++t) {
-          if (t < t_end) {
+        for (int t = 0; t <= n; ++t) {
+          if (t < n) {
             const int b = t & 1, slot = t % DQ_KS;
             if (!wait_bar_all(&sm.kv_full[slot], (t / DQ_KS) & 1, wc)) break;
-            // buffer b was last read by the first pass (the second one's use is waited for below)
-            if (CKPT && t >= 2 && t - 2 < t_dq && !wait_bar_all(&sm.ds_full[b], ((t - 2) >> 1) & 1, wc)) break;
             tc_fence_after();
             const uint32_t kb = smem_u32(sm.k[slot][0]), vb = smem_u32(sm.v[slot][0]);
 #pragma unroll
@@ -748,9 +725,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
                         kk > 0 ? 1u : 0u);
             }
             mma_commit_el(&sm.sdp_full[b]);
-            if (CKPT && t < t_dq) mma_commit_el(&sm.kv_empty[slot]);
           }
-          if (t >= t_dq + 1) {
+          if (t >= 1) {
             const int u = t - 1, b = u & 1, slot = u % DQ_KS;
             if (!wait_bar_all(&sm.ds_full[b], (u >> 1) & 1, wc)) break;
             tc_fence_after();
@@ -760,8 +736,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 mma_ts_el(tmem + T_DQ, tmem + T_S + b * 64 + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
-                          sdesc_sw128(kb + kk * 2048, 64 * 128, 1024), IDESC_Q,
-                          (u > t_dq || part > 0 || kk > 0) ? 1u : 0u);
+                          sdesc_sw128(kb + kk * 2048, 64 * 128, 1024), IDESC_Q, (u > 0 || part > 0 || kk > 0) ? 1u : 0u);
             }
             mma_commit_el(&sm.kv_empty[slot]);
           }
@@ -780,41 +755,19 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
     const bool rvalid = row < N;
     // Q_i (warpgroup 0) and dO_i (warpgroup 1) into TMEM, one row per thread
     {
+      const uint4* src = h == 0 ? reinterpret_cast<const uint4*>(qg + ((long long)bh * N + row) * D)
+                                : reinterpret_cast<const uint4*>(dout + ((long long)bh * N + row) * D);
       // every load of the row first (one memory round trip), then the TMEM stores
       uint32_t w[D / 64][32];
-      if (CKPT && h == 0) {
-        uint4 code[D / 16];
-        uint8_t E[D / 32];
-        const long long at = (long long)bh * N + row;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c)
-          code[c] = rvalid ? reinterpret_cast<const uint4*>(q8 + at * D)[c] : make_uint4(0, 0, 0, 0);
+      for (int c = 0; c < D / 64; ++c) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) E[c] = rvalid ? qe[at * (D / 32) + c] : (uint8_t)0;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const float step = pack8_step(E[c >> 1]);
-          const uint32_t* x = reinterpret_cast<const uint32_t*>(&code[c]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t two = x[e >> 1] >> (16 * (e & 1));
-            w[c >> 2][8 * (c & 3) + e] = pack_bf16(static_cast<float>((int8_t)two) * step,
-                                                   static_cast<float>((int8_t)(two >> 8)) * step);
-          }
-        }
-      } else {
-        const uint4* src = h == 0 ? reinterpret_cast<const uint4*>(qg + ((long long)bh * N + row) * D)
-                                  : reinterpret_cast<const uint4*>(dout + ((long long)bh * N + row) * D);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 x = rvalid ? src[c * 8 + e] : make_uint4(0, 0, 0, 0);
-            w[c][4 * e] = x.x;
-            w[c][4 * e + 1] = x.y;
-            w[c][4 * e + 2] = x.z;
-            w[c][4 * e + 3] = x.w;
-          }
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = rvalid ? src[c * 8 + e] : make_uint4(0, 0, 0, 0);
+          w[c][4 * e] = x.x;
+          w[c][4 * e + 1] = x.y;
+          w[c][4 * e + 2] = x.z;
+          w[c][4 * e + 3] = x.w;
         }
       }
 #pragma unroll
@@ -823,88 +776,16 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
       tc_fence_before();
       mbar_arrive(&sm.qd_ready);
     }
+    const float nlse2 = rvalid ? -lse[(long long)bh * N + row] * LOG2E : -INFINITY;
+    const float Dr = rvalid ? dvec[(long long)bh * N + row] : 0.f;
+    const uint64_t scale2 = f2_pack(scale_log2, scale_log2), nlse2x2 = f2_pack(nlse2, nlse2),
+                   d2 = f2_pack(Dr, Dr);
     // only kv-block Tn-1 (last in the ascending list) is ragged
     const int last_valid = (n > 0 && (kv_list[n - 1] & TILE_ID_MASK) == Tn - 1) ? N - (Tn - 1) * 64 : 64;
     bool ok = n > 0;
-    float nlse2 = -INFINITY, Dr = 0.f;
-    if constexpr (CKPT) {
-      // ---- first pass: LSE and D of the row, from its 32 columns of every tile
-      float m = -INFINITY, l = 0.f, wsum = 0.f;
-      for (int t = 0; t < n && ok; ++t) {
-        const int b = t & 1;
-        if (!wait_warp(&sm.sdp_full[b], (t >> 1) & 1, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const int kv_valid = (TILED && tile_excluded(kv_list[t], r >> 6)) ? 0 : t == n - 1 ? last_valid : 64;
-        const int c0 = h * 32;
-        uint32_t sa[32], pa[32];
-        tmem_ld32(tl + T_S + b * 64 + c0, sa);
-        tmem_ld32(tl + T_DP + b * 64 + c0, pa);
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(&sm.ds_full[b]);  // the buffer may be overwritten
-        if (kv_valid < 64) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c0 + e >= kv_valid) sa[e] = __float_as_uint(-INFINITY);
-        }
-        float m4[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m4[e] = __uint_as_float(sa[e]);
-#pragma unroll
-        for (int e = 4; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sa[e]));
-        const float m_new = fmaxf(m, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale_log2);
-        if (m_new == -INFINITY) continue;  // nothing kept so far in these columns
-        const float alpha = fast_exp2(m - m_new);
-        m = m_new;
-        const uint64_t neg_m = f2_pack(-m_new, -m_new), sc2 = f2_pack(scale_log2, scale_log2);
-        float l2[2] = {l * alpha, 0.f}, w2[2] = {wsum * alpha, 0.f};
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float x0, x1;
-          f2_unpack(f2_fma(f2_pack(__uint_as_float(sa[2 * e]), __uint_as_float(sa[2 * e + 1])), sc2, neg_m), x0, x1);
-          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-          l2[0] += p0;
-          l2[1] += p1;
-          w2[0] = fmaf(p0, __uint_as_float(pa[2 * e]), w2[0]);
-          w2[1] = fmaf(p1, __uint_as_float(pa[2 * e + 1]), w2[1]);
-        }
-        l = l2[0] + l2[1];
-        wsum = w2[0] + w2[1];
-      }
-      if (n > 0) {
-        sm.part[h][0][r] = m;
-        sm.part[h][1][r] = l;
-        sm.part[h][2][r] = wsum;
-        named_bar_sync(1, 256);
-        const float mo = sm.part[1 - h][0][r], M = fmaxf(m, mo);
-        if (M > -INFINITY) {
-          const float a0 = fast_exp2(m - M), a1 = fast_exp2(mo - M);
-          l = fmaf(l, a0, sm.part[1 - h][1][r] * a1);
-          wsum = fmaf(wsum, a0, sm.part[1 - h][2][r] * a1);
-          nlse2 = -(M + log2f(l));
-          Dr = wsum / l;
-        }
-        if (h == 0 && rvalid && ok) {  // +inf: a row that keeps nothing, as the dK/dV pass takes it
-          lse[(long long)bh * N + row] = -nlse2 * 0.69314718055994530942f;
-          dvec[(long long)bh * N + row] = Dr;
-        }
-        if (!rvalid) {
-          nlse2 = -INFINITY;
-          Dr = 0.f;
-        }
-      }
-    } else if (rvalid) {
-      nlse2 = -lse[(long long)bh * N + row] * LOG2E;
-      Dr = dvec[(long long)bh * N + row];
-    }
-    const uint64_t scale2 = f2_pack(scale_log2, scale_log2), nlse2x2 = f2_pack(nlse2, nlse2),
-                   d2 = f2_pack(Dr, Dr);
     for (int t = 0; t < n && ok; ++t) {
-      const int g = t_dq + t, b = g & 1;
-      if (!wait_warp(&sm.sdp_full[b], (g >> 1) & 1, wc)) {
+      const int b = t & 1;
+      if (!wait_warp(&sm.sdp_full[b], (t >> 1) & 1, wc)) {
         ok = false;
         break;
       }
@@ -1043,9 +924,10 @@ SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* 
   __syncthreads();  // start[] is reused by the next head of this block
 }
 
-// D = rowsum(dO * (O + O_lo)) in fp32; fp16 copies of the dO and Q rows (CKPT: of the dO
-// rows, and no D: the dQ pass finds it, and Q's copy comes with its decoding)
+// D = rowsum(dO * (O + O_lo)) in fp32; fp16 copies of the dO and Q rows
 // (|x| > 65504 clamped and reported). D / 8 threads per row, 16-byte accesses.
+// CKPT (the backward on 8-bit checkpoints): dO's copy only; the dQ pass finds D,
+// and Q's copy comes with its decoding.
 // Blocks 0 .. BH-1 (each a stride of heads, when there are fewer blocks) also
 // write the order in which the dK/dV pass takes its columns.
 template <int D, bool CKPT>
@@ -1111,6 +993,19 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __res
   for (int head = blockIdx.x; head < BH; head += gridDim.x) longest_first(col_cnt, Tn, head, col_order);
 }
 
+// 1. D and the fp16 copies of dO and Q
+template <int D, bool CKPT>
+static cudaError_t launch_pre(const BwdArgs& a, cudaStream_t s) {
+  const long long rows = (long long)a.BH * a.N;
+  constexpr int PRE_ROWS = 256 / (D / 8);  // rows per 256-thread block
+  KernelTimer kt(KID_BWD_PRE, s);
+  bwd_pre_kernel<D, CKPT><<<(unsigned)((rows + PRE_ROWS - 1) / PRE_ROWS), 256, 0, s>>>(
+      (const __nv_bfloat16*)a.o, (const __nv_bfloat16*)a.o_lo, (const __nv_bfloat16*)a.dout, (const __nv_bfloat16*)a.q,
+      a.dvec, (uint32_t*)a.do16, (uint32_t*)a.q16, rows, a.col_cnt, a.BH, a.Tn, a.col_order, a.status);
+  return cudaGetLastError();
+}
+
+// 2. dK, dV (kv-major)
 template <int D, bool TILED>
 static cudaError_t launch_dkdv(const BwdArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(BwdSmem<D>) + 1024;
@@ -1128,51 +1023,37 @@ static cudaError_t launch_dkdv(const BwdArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, bool TILED, bool CKPT>
+// 3. dQ (q-major)
+template <int D, bool TILED>
 static cudaError_t launch_dq(const BwdArgs& a, cudaStream_t s) {
-  const size_t smem = sizeof(DqSmem<D, CKPT>) + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(bwd_dq_kernel<D, TILED, CKPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const size_t smem = sizeof(DqSmem<D>) + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(bwd_dq_kernel<D, TILED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
   if (e != cudaSuccess) return e;
   KernelTimer kt(KID_BWD_DQ, s);
-  bwd_dq_kernel<D, TILED, CKPT><<<dim3(a.Tm, a.BH), DQ_THREADS, smem, s>>>(
-      *a.tm_k, *a.tm_v, *a.tm_dq, static_cast<const __nv_bfloat16*>(a.q), a.q8, a.qe,
-      static_cast<const __nv_bfloat16*>(a.dout), a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N, a.Tm, a.Tn,
-      a.scale, a.scale_log2, a.status, a.wait_limit_ns);
+  bwd_dq_kernel<D, TILED><<<dim3(a.Tm, a.BH), DQ_THREADS, smem, s>>>(
+      *a.tm_k, *a.tm_v, *a.tm_dq, static_cast<const __nv_bfloat16*>(a.q), static_cast<const __nv_bfloat16*>(a.dout),
+      a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N, a.Tm, a.Tn, a.scale, a.scale_log2, a.status,
+      a.wait_limit_ns);
   return cudaGetLastError();
 }
 
-template <int D, bool TILED, bool CKPT>
+template <int D, bool TILED>
 static cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t s) {
-  const long long rows = (long long)a.BH * a.N;
-  // 1. D and the fp16 copies of dO and Q
-  constexpr int PRE_ROWS = 256 / (D / 8);  // rows per 256-thread block
-  {
-    KernelTimer kt(KID_BWD_PRE, s);
-    bwd_pre_kernel<D, CKPT><<<(unsigned)((rows + PRE_ROWS - 1) / PRE_ROWS), 256, 0, s>>>(
-        (const __nv_bfloat16*)a.o, (const __nv_bfloat16*)a.o_lo, (const __nv_bfloat16*)a.dout,
-        (const __nv_bfloat16*)a.q, a.dvec, (uint32_t*)a.do16, (uint32_t*)a.q16, rows, a.col_cnt, a.BH, a.Tn,
-        a.col_order, a.status);
+  cudaError_t e;
+  if (a.q8) {  // the dQ pass finds LSE and D, so it goes before dK, dV
+    if ((e = launch_pre<D, true>(a, s)) != cudaSuccess) return e;
+    if ((e = launch_dq_ckpt(a, D, s)) != cudaSuccess) return e;
+    return launch_dkdv<D, TILED>(a, s);
   }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // 2. and 3. dK, dV (kv-major) and dQ (q-major); on checkpoints dQ first, which finds LSE and D
-  if (CKPT) {
-    e = launch_dq<D, TILED, CKPT>(a, s);
-    return e != cudaSuccess ? e : launch_dkdv<D, TILED>(a, s);
-  }
-  e = launch_dkdv<D, TILED>(a, s);
-  return e != cudaSuccess ? e : launch_dq<D, TILED, CKPT>(a, s);
-}
-
-template <int D>
-static cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t s) {
-  if (a.q8) return a.tiled ? launch_bwd_d<D, true, true>(a, s) : launch_bwd_d<D, false, true>(a, s);
-  return a.tiled ? launch_bwd_d<D, true, false>(a, s) : launch_bwd_d<D, false, false>(a, s);
+  if ((e = launch_pre<D, false>(a, s)) != cudaSuccess) return e;
+  if ((e = launch_dkdv<D, TILED>(a, s)) != cudaSuccess) return e;
+  return launch_dq<D, TILED>(a, s);
 }
 
 cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s) {
-  return d == 128 ? launch_bwd_t<128>(a, s) : launch_bwd_t<64>(a, s);
+  if (d == 128) return a.tiled ? launch_bwd_d<128, true>(a, s) : launch_bwd_d<128, false>(a, s);
+  return a.tiled ? launch_bwd_d<64, true>(a, s) : launch_bwd_d<64, false>(a, s);
 }
 
 }  // namespace spa2

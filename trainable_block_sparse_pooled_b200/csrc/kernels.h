@@ -26,6 +26,7 @@ enum KernelId : int {
   KID_ROTARY,
   KID_PACK8,
   KID_UNPACK8,
+  KID_BWD_DQ_CKPT,
   KID_COUNT
 };
 
@@ -122,8 +123,12 @@ struct BwdArgs {
   // are the kept values
   const int8_t* q8;
   const uint8_t* qe;
+  const CUtensorMap* tm_dob;  // dO bf16, box {64, 128, 1}
 };
 cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s);
+
+// attn_bwd_ckpt.cu: the dQ pass on 8-bit checkpoints, which also finds LSE and D
+cudaError_t launch_dq_ckpt(const BwdArgs& a, int d, cudaStream_t s);
 
 // pack8.cu: 8-bit groups (checked arguments), x -> codes, exps or back. f16, where given, holds
 // for each tensor null or a place for an fp16 copy of x (of the values, unpacking), which

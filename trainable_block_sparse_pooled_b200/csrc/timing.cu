@@ -29,6 +29,7 @@ const char* const kNames[KID_COUNT] = {
     "rotary_kernel",      // KID_ROTARY
     "pack8_kernel",       // KID_PACK8
     "unpack8_kernel",     // KID_UNPACK8
+    "bwd_dq_ckpt_kernel", // KID_BWD_DQ_CKPT
 };
 
 struct Record {
