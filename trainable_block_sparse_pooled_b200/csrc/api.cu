@@ -497,8 +497,7 @@ spa2_status spa2_sparse_attn_fwd_ckpt(const void* q, const void* k, const void* 
   const spa2_pack8_tensor t[3] = {{const_cast<void*>(q), q8->codes, q8->exps, rows, d},
                                   {const_cast<void*>(k), k8->codes, k8->exps, rows, d},
                                   {const_cast<void*>(v), v8->codes, v8->exps, rows, d}};
-  void* const f16[3] = {nullptr, nullptr, w.v16};
-  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, false, st, f16, w.status));
+  SPA2_CUDA_TRY(launch_pack8_step(t, w.v16, w.status, st));
   FwdArgs a{&tq, &tk, &tv, &to, &to, 0, rc, ri, lse, (int)s.BH, s.N, s.TMt, s.TNt,
             scale * 1.4426950408889634f, w.status, g_wait_limit_ns, s.tiled ? 1 : 0};
   SPA2_CUDA_TRY(launch_fwd(a, d, st));
@@ -542,11 +541,8 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
     ci = t.csc_idx;
   }
   const long long rows = s.BH * s.N;
-  const spa2_pack8_tensor t[3] = {{nullptr, q8->codes, q8->exps, rows, d},
-                                  {w.k, k8->codes, k8->exps, rows, d},
-                                  {w.v, v8->codes, v8->exps, rows, d}};
-  void* const f16[3] = {w.b.q16, nullptr, nullptr};
-  SPA2_CUDA_TRY(launch_pack8(t, 3, SPA2_DTYPE_BF16, true, st, f16, status));
+  const spa2_pack8_tensor t[2] = {{w.k, k8->codes, k8->exps, rows, d}, {w.v, v8->codes, v8->exps, rows, d}};
+  SPA2_CUDA_TRY(launch_unpack8_step(t, ColumnOrder{cc, (int)s.BH, s.TNt, w.b.col_order}, st));
   BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, w.k, nullptr, nullptr, dout, w.v, w.lse, rc, ri, cc, ci,
             w.b.dvec, w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
             scale * 1.4426950408889634f, status, status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.b.col_order,

@@ -877,60 +877,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1) bwd_dq_kernel(const __grid_cons
   }
 }
 
-// One head's kv columns (Tn counts from head * Tn on), longest first, written
-// as global column indices head * Tn + c: a counting sort by one 256-thread
-// block (keys clamped to [0, 1023]; the order among equal counts is whatever the
-// shared-memory atomics give, which does not matter: a column's gradients are
-// computed the same way whichever CTA takes it and whenever). The persistent
-// dK/dV pass takes its columns head by head and, within a head, long columns
-// first: it does not end on a long column, and the Q / dO tiles the running
-// columns share stay within one head's worth of L2.
-SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* __restrict__ order) {
-  constexpr int KEYS = 1024, PER = KEYS / 256;
-  __shared__ int start[KEYS];
-  __shared__ int warp_sum[8];
-  const int t = threadIdx.x;
-  const int* cnt_h = cnt + (long long)head * Tn;
-  int* out_h = order + (long long)head * Tn;
-  for (int k = t; k < KEYS; k += 256) start[k] = 0;
-  __syncthreads();
-  for (int c = t; c < Tn; c += 256) atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
-  __syncthreads();
-  // exclusive scan in descending key order: thread t owns keys KEYS-1-PER*t ... KEYS-PER-PER*t
-  int bin[PER], sum = 0;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    bin[e] = start[KEYS - 1 - PER * t - e];
-    sum += bin[e];
-  }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if ((t & 31) >= o) incl += y;
-  }
-  if ((t & 31) == 31) warp_sum[t >> 5] = incl;
-  __syncthreads();
-  int base = incl - sum;
-  for (int w = 0; w < (t >> 5); ++w) base += warp_sum[w];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) {
-    start[KEYS - 1 - PER * t - e] = base;
-    base += bin[e];
-  }
-  __syncthreads();
-  for (int c = t; c < Tn; c += 256)
-    out_h[atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1)] = head * Tn + c;
-  __syncthreads();  // start[] is reused by the next head of this block
-}
-
 // D = rowsum(dO * (O + O_lo)) in fp32; fp16 copies of the dO and Q rows
 // (|x| > 65504 clamped and reported). D / 8 threads per row, 16-byte accesses.
-// CKPT (the backward on 8-bit checkpoints): dO's copy only; the dQ pass finds D,
-// and Q's copy comes with its decoding.
 // Blocks 0 .. BH-1 (each a stride of heads, when there are fewer blocks) also
 // write the order in which the dK/dV pass takes its columns.
-template <int D, bool CKPT>
+template <int D>
 __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __restrict__ o,
                                                       const __nv_bfloat16* __restrict__ o_lo,
                                                       const __nv_bfloat16* __restrict__ dout,
@@ -948,11 +899,10 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __res
   bool bad = false;
   if (row < rows) {
     const long long off = row * D + tc * 8;
-    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 ow = CKPT ? none : *reinterpret_cast<const uint4*>(o + off);
-    const uint4 lw = !CKPT && o_lo ? *reinterpret_cast<const uint4*>(o_lo + off) : none;
+    const uint4 ow = *reinterpret_cast<const uint4*>(o + off);
+    const uint4 lw = o_lo ? *reinterpret_cast<const uint4*>(o_lo + off) : make_uint4(0u, 0u, 0u, 0u);
     const uint4 bw = *reinterpret_cast<const uint4*>(dout + off);
-    const uint4 qw = CKPT ? none : *reinterpret_cast<const uint4*>(q + off);
+    const uint4 qw = *reinterpret_cast<const uint4*>(q + off);
     const uint32_t* O = reinterpret_cast<const uint32_t*>(&ow);
     const uint32_t* L = reinterpret_cast<const uint32_t*>(&lw);
     const uint32_t* Bd = reinterpret_cast<const uint32_t*>(&bw);
@@ -982,24 +932,22 @@ __global__ void __launch_bounds__(256) bwd_pre_kernel(const __nv_bfloat16* __res
     }
     const long long w = off / 2;  // 32-bit word of the fp16 copies
     *reinterpret_cast<uint4*>(do16 + w) = make_uint4(d16[0], d16[1], d16[2], d16[3]);
-    if (!CKPT) *reinterpret_cast<uint4*>(q16 + w) = make_uint4(q16w[0], q16w[1], q16w[2], q16w[3]);
+    *reinterpret_cast<uint4*>(q16 + w) = make_uint4(q16w[0], q16w[1], q16w[2], q16w[3]);
   }
-  if constexpr (!CKPT) {
 #pragma unroll
-    for (int s = TPR / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffff, acc, s);
-    if (row < rows && tc == 0) dvec[row] = acc;
-  }
+  for (int s = TPR / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffff, acc, s);
+  if (row < rows && tc == 0) dvec[row] = acc;
   if (bad) report(status, SPA2_ERR_RANGE);
   for (int head = blockIdx.x; head < BH; head += gridDim.x) longest_first(col_cnt, Tn, head, col_order);
 }
 
 // 1. D and the fp16 copies of dO and Q
-template <int D, bool CKPT>
+template <int D>
 static cudaError_t launch_pre(const BwdArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.BH * a.N;
   constexpr int PRE_ROWS = 256 / (D / 8);  // rows per 256-thread block
   KernelTimer kt(KID_BWD_PRE, s);
-  bwd_pre_kernel<D, CKPT><<<(unsigned)((rows + PRE_ROWS - 1) / PRE_ROWS), 256, 0, s>>>(
+  bwd_pre_kernel<D><<<(unsigned)((rows + PRE_ROWS - 1) / PRE_ROWS), 256, 0, s>>>(
       (const __nv_bfloat16*)a.o, (const __nv_bfloat16*)a.o_lo, (const __nv_bfloat16*)a.dout, (const __nv_bfloat16*)a.q,
       a.dvec, (uint32_t*)a.do16, (uint32_t*)a.q16, rows, a.col_cnt, a.BH, a.Tn, a.col_order, a.status);
   return cudaGetLastError();
@@ -1041,12 +989,11 @@ static cudaError_t launch_dq(const BwdArgs& a, cudaStream_t s) {
 template <int D, bool TILED>
 static cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t s) {
   cudaError_t e;
-  if (a.q8) {  // the dQ pass finds LSE and D, so it goes before dK, dV
-    if ((e = launch_pre<D, true>(a, s)) != cudaSuccess) return e;
+  if (a.q8) {  // the dQ pass finds LSE and D and writes the fp16 copies, so it goes first
     if ((e = launch_dq_ckpt(a, D, s)) != cudaSuccess) return e;
     return launch_dkdv<D, TILED>(a, s);
   }
-  if ((e = launch_pre<D, false>(a, s)) != cudaSuccess) return e;
+  if ((e = launch_pre<D>(a, s)) != cudaSuccess) return e;
   if ((e = launch_dkdv<D, TILED>(a, s)) != cudaSuccess) return e;
   return launch_dq<D, TILED>(a, s);
 }

@@ -11,7 +11,8 @@
 //     second  S and dP again, dS = P * (dP - D), dQ_i += dS K_j * scale, as in
 //             bwd_dq_kernel: dS as a hi + lo pair of bf16 values in tensor memory.
 //   Q_i is decoded from its codes into shared memory, dO_i, K_j and V_j (the kept values in
-//   bf16) arrive by TMA.
+//   bf16) arrive by TMA. The fp16 copies of Q and dO that the dK/dV pass streams are written
+//   from here as well (|x| > 65504 clamped and reported).
 //
 // What bounds it: each product chain of a CTA is serial (S and dP have one buffer each, dS
 // goes over S), so a second CTA on the SM works through its own chain meanwhile, and through
@@ -64,7 +65,8 @@ template <int D, bool TILED>
 __global__ void __launch_bounds__(DQC_THREADS, 2)
     bwd_dq_ckpt_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
-                       const int8_t* __restrict__ q8, const uint8_t* __restrict__ qe, float* __restrict__ lse,
+                       const int8_t* __restrict__ q8, const uint8_t* __restrict__ qe, uint4* __restrict__ q16,
+                       uint4* __restrict__ do16, float* __restrict__ lse,
                        float* __restrict__ dvec, const int* __restrict__ row_cnt, const int* __restrict__ row_idx,
                        int grad_f32, int N, int Tm, int Tn, float scale, float scale_log2, int* status,
                        unsigned long long wait_limit_ns) {
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     // Q_i from its codes: 16 elements of a row at a time, neighbours in neighbouring threads
     {
       constexpr int PER_ROW = D / 16, PIECES = 128 * PER_ROW / 256;
+      bool bad = false;
       uint4 code[PIECES];
       uint8_t E[PIECES];
 #pragma unroll
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
         const int piece = x * 256 + threadIdx.x, pr = piece / PER_ROW, c = piece % PER_ROW;
         const float step = pack8_step(E[x]);
         const uint32_t in[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
-        uint32_t w[8];
+        uint32_t w[8], w16[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float f[4];
@@ -282,6 +285,13 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
           // codes of rows behind the last are 0, which the conversion takes for +0
           w[2 * e] = pack_bf16(f[0] * step, f[1] * step);
           w[2 * e + 1] = pack_bf16(f[2] * step, f[3] * step);
+          w16[2 * e] = pack_f16_clamped(f[0] * step, f[1] * step, bad);
+          w16[2 * e + 1] = pack_f16_clamped(f[2] * step, f[3] * step, bad);
+        }
+        if (i * 128 + pr < N) {
+          uint4* to = q16 + (((long long)bh * N + (long long)i * 128 + pr) * D + c * 16) / 8;
+          to[0] = make_uint4(w16[0], w16[1], w16[2], w16[3]);
+          to[1] = make_uint4(w16[4], w16[5], w16[6], w16[7]);
         }
         uint8_t* chunk = sm.q[c >> 2];
         *reinterpret_cast<uint4*>(chunk + sw128_offset(pr, (c & 3) * 2)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -289,6 +299,22 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       }
       fence_proxy_async_smem();
       mbar_arrive(&sm.q_ready);
+      // fp16 copy of dO_i, 8 elements of a row at a time
+      if (n > 0 && wait_warp(&sm.do_full, 0, wc)) {
+#pragma unroll
+        for (int x = 0; x < 128 * D / 8 / 256; ++x) {
+          const int piece = x * 256 + threadIdx.x, pr = piece / (D / 8), c = piece % (D / 8);
+          if (i * 128 + pr >= N) continue;
+          const uint4 in = *reinterpret_cast<const uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7));
+          auto to16 = [&bad](uint32_t w) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+            return pack_f16_clamped(f.x, f.y, bad);
+          };
+          do16[(((long long)bh * N + (long long)i * 128 + pr) * D) / 8 + c] =
+              make_uint4(to16(in.x), to16(in.y), to16(in.z), to16(in.w));
+        }
+      }
+      if (bad) report(status, SPA2_ERR_RANGE);
     }
     const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
     // only kv-block Tn-1 (last in the ascending list) is ragged
@@ -478,7 +504,7 @@ static cudaError_t launch_dq_ckpt_t(const BwdArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   KernelTimer kt(KID_BWD_DQ_CKPT, s);
   bwd_dq_ckpt_kernel<D, TILED><<<dim3(a.Tm, a.BH), DQC_THREADS, smem, s>>>(
-      *a.tm_dob, *a.tm_k, *a.tm_v, *a.tm_dq, a.q8, a.qe, a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N, a.Tm, a.Tn,
+      *a.tm_dob, *a.tm_k, *a.tm_v, *a.tm_dq, a.q8, a.qe, static_cast<uint4*>(a.q16), static_cast<uint4*>(a.do16), a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N, a.Tm, a.Tn,
       a.scale, a.scale_log2, a.status, a.wait_limit_ns);
   return cudaGetLastError();
 }

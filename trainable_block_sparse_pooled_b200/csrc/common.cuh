@@ -511,4 +511,51 @@ SPA2_DEV float fast_exp2(float x) {
   return y;
 }
 
+// One head's kv columns (Tn counts from head * Tn on), longest first, written
+// as global column indices head * Tn + c: a counting sort by one 256-thread
+// block (keys clamped to [0, 1023]; the order among equal counts is whatever the
+// shared-memory atomics give, which does not matter: a column's gradients are
+// computed the same way whichever CTA takes it and whenever). The persistent
+// dK/dV pass takes its columns head by head and, within a head, long columns
+// first: it does not end on a long column, and the Q / dO tiles the running
+// columns share stay within one head's worth of L2.
+SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* __restrict__ order) {
+  constexpr int KEYS = 1024, PER = KEYS / 256;
+  __shared__ int start[KEYS];
+  __shared__ int warp_sum[8];
+  const int t = threadIdx.x;
+  const int* cnt_h = cnt + (long long)head * Tn;
+  int* out_h = order + (long long)head * Tn;
+  for (int k = t; k < KEYS; k += 256) start[k] = 0;
+  __syncthreads();
+  for (int c = t; c < Tn; c += 256) atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
+  __syncthreads();
+  // exclusive scan in descending key order: thread t owns keys KEYS-1-PER*t ... KEYS-PER-PER*t
+  int bin[PER], sum = 0;
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    bin[e] = start[KEYS - 1 - PER * t - e];
+    sum += bin[e];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if ((t & 31) >= o) incl += y;
+  }
+  if ((t & 31) == 31) warp_sum[t >> 5] = incl;
+  __syncthreads();
+  int base = incl - sum;
+  for (int w = 0; w < (t >> 5); ++w) base += warp_sum[w];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    start[KEYS - 1 - PER * t - e] = base;
+    base += bin[e];
+  }
+  __syncthreads();
+  for (int c = t; c < Tn; c += 256)
+    out_h[atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1)] = head * Tn + c;
+  __syncthreads();  // start[] is reused by the next head of this block
+}
+
 }  // namespace spa2

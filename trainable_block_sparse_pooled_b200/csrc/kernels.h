@@ -119,8 +119,8 @@ struct BwdArgs {
   unsigned long long wait_limit_ns;
   int tiled;          // list entries may carry tile exclusion bits
   int* col_order;     // [BH * Tn]: the dK/dV pass's columns, head by head, long columns first (pre-pass)
-  // on 8-bit checkpoints (otherwise null): Q's codes and exponents; q16 is already there, k and v
-  // are the kept values
+  // on 8-bit checkpoints (otherwise null): Q's codes and exponents; col_order is already there, k and
+  // v are the kept values, and the dQ pass writes lse, dvec, do16 and q16
   const int8_t* q8;
   const uint8_t* qe;
   const CUtensorMap* tm_dob;  // dO bf16, box {64, 128, 1}
@@ -130,11 +130,16 @@ cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s);
 // attn_bwd_ckpt.cu: the dQ pass on 8-bit checkpoints, which also finds LSE and D
 cudaError_t launch_dq_ckpt(const BwdArgs& a, int d, cudaStream_t s);
 
-// pack8.cu: 8-bit groups (checked arguments), x -> codes, exps or back. f16, where given, holds
-// for each tensor null or a place for an fp16 copy of x (of the values, unpacking), which
-// needs rows of whole 16-byte units; |x| > 65504 is clamped and reported to status.
-cudaError_t launch_pack8(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, cudaStream_t s,
-                         void* const* f16 = nullptr, int* status = nullptr);
+// pack8.cu. The checkpoints of a step's q, k, v [rows, d] bf16 (d = 64 or 128, 16-byte aligned),
+// with an fp16 copy of v; |v| > 65504 is clamped and reported to status
+cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* status, cudaStream_t s);
+// and the kept values of k, v, with the order in which the dK/dV pass takes its columns
+struct ColumnOrder {
+  const int* cnt;  // [heads, Tn] column counts
+  int heads, Tn;
+  int* out;        // BwdArgs::col_order
+};
+cudaError_t launch_unpack8_step(const spa2_pack8_tensor (&t)[2], const ColumnOrder& order, cudaStream_t s);
 
 // api.cu
 cudaError_t launch_timeout_probe(int* status, unsigned long long limit_ns, cudaStream_t s);

@@ -20,11 +20,14 @@ namespace spa2 {
 namespace {
 
 struct Pack8Args {
-  spa2_pack8_tensor t[SPA2_PACK8_MAX];  // unpacking with f16, x may be null
-  uint32_t* f16[SPA2_PACK8_MAX];        // fp16 copy of the tensor (packing) or of its values, or null
+  spa2_pack8_tensor t[SPA2_PACK8_MAX];
+  uint32_t* f16[SPA2_PACK8_MAX];        // packing: fp16 copy of the tensor, or null
   int* status;                          // where |x| > 65504 is reported; needed for a copy
   uint32_t per_row[SPA2_PACK8_MAX];     // chunk places of a row, and x / per_row = x * div_mul >> (32 + div_shift)
   uint32_t div_mul[SPA2_PACK8_MAX], div_shift[SPA2_PACK8_MAX];  // for x < 2^31
+  // ORDER: the blocks beyond the n tensors write the order in which the dK/dV pass takes its columns
+  int n;
+  ColumnOrder order;
 };
 
 constexpr int CHUNK = 8, PER_GROUP = 4, UNROLL = 4, THREADS = 256;
@@ -88,8 +91,8 @@ SPA2_DEV uint32_t chunk_exponent(const Chunk<T>& x) {
   }
 }
 
-// fp16 copy of a chunk; below 2^16 (E <= 142) only fp32 inputs could exceed 65504 by rounding,
-// and copies are made of bf16 tensors and of codes (7 bits): no element needs a look
+// fp16 copy of a chunk of a bf16 tensor; below 2^16 (E <= 142) bf16 values are at most 65280 and
+// no element needs a look
 SPA2_DEV void store_f16(uint32_t* to, const float (&f)[CHUNK], uint32_t E, bool& bad) {
   uint4 w;
   if (E <= 142u)
@@ -145,13 +148,17 @@ __global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) pack8
   if (bad) report(a.status, SPA2_ERR_RANGE);
 }
 
-template <typename T, bool FLAT>
+template <typename T, bool FLAT, bool ORDER>
 __global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) unpack8_kernel(const __grid_constant__ Pack8Args a) {
+  if (ORDER && blockIdx.y == a.n) {
+    for (int head = blockIdx.x; head < a.order.heads; head += gridDim.x)
+      longest_first(a.order.cnt, a.order.Tn, head, a.order.out);
+    return;
+  }
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
   const Places<FLAT> places(a);
-  uint32_t* f16 = a.f16[blockIdx.y];
   long long e[UNROLL], group;
-  bool here[UNROLL], bad = false;
+  bool here[UNROLL];
   uint2 code[UNROLL];
   uint8_t E[UNROLL];
 #pragma unroll
@@ -166,19 +173,14 @@ __global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) unpac
   for (int u = 0; u < UNROLL; ++u) {
     if (!here[u]) continue;
     const float step = pack8_step(E[u]);
-    float lo[4], hi[4], f[CHUNK];
+    float lo[4], hi[4];
     pack8_floats(code[u].x, lo);
     pack8_floats(code[u].y, hi);
     Chunk<T> x;
 #pragma unroll
-    for (int i = 0; i < CHUNK; ++i) {
-      f[i] = (i < 4 ? lo[i & 3] : hi[i & 3]) * step;
-      x.e[i] = static_cast<T>(f[i]);
-    }
-    if (t.x) *reinterpret_cast<Chunk<T>*>(static_cast<T*>(t.x) + e[u]) = x;
-    if (f16) store_f16(f16 + e[u] / 2, f, E[u], bad);
+    for (int i = 0; i < CHUNK; ++i) x.e[i] = static_cast<T>((i < 4 ? lo[i & 3] : hi[i & 3]) * step);
+    *reinterpret_cast<Chunk<T>*>(static_cast<T*>(t.x) + e[u]) = x;
   }
-  if (bad) report(a.status, SPA2_ERR_RANGE);
 }
 
 // one warp per group, one lane per element
@@ -231,7 +233,7 @@ static cudaError_t launch_pack8_t(Pack8Args& a, int n, bool unpack, cudaStream_t
   KernelTimer kt(unpack ? KID_UNPACK8 : KID_PACK8, s);
   if (chunks) {
     const dim3 grid((unsigned)((groups * PER_GROUP + PLACES - 1) / PLACES), (unsigned)n);
-    auto* k = unpack ? (flat ? unpack8_kernel<T, true> : unpack8_kernel<T, false>)
+    auto* k = unpack ? (flat ? unpack8_kernel<T, true, false> : unpack8_kernel<T, false, false>)
                      : (flat ? pack8_kernel<T, true> : pack8_kernel<T, false>);
     k<<<grid, THREADS, 0, s>>>(a);
   } else {
@@ -241,17 +243,29 @@ static cudaError_t launch_pack8_t(Pack8Args& a, int n, bool unpack, cudaStream_t
   return cudaGetLastError();
 }
 
-cudaError_t launch_pack8(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, cudaStream_t s, void* const* f16,
-                         int* status) {
-  Pack8Args a{};
-  for (int i = 0; i < n; ++i) {
-    a.t[i] = t[i];
-    a.f16[i] = f16 ? static_cast<uint32_t*>(f16[i]) : nullptr;
-  }
-  a.status = status;
+static cudaError_t launch(Pack8Args& a, int n, int dtype, bool unpack, cudaStream_t s) {
   return dtype == SPA2_DTYPE_BF16  ? launch_pack8_t<__nv_bfloat16>(a, n, unpack, s)
          : dtype == SPA2_DTYPE_F16 ? launch_pack8_t<__half>(a, n, unpack, s)
                                    : launch_pack8_t<float>(a, n, unpack, s);
+}
+
+cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* status, cudaStream_t s) {
+  Pack8Args a{};
+  std::copy(t, t + 3, a.t);
+  a.f16[2] = static_cast<uint32_t*>(v16);
+  a.status = status;
+  return launch(a, 3, SPA2_DTYPE_BF16, false, s);
+}
+
+cudaError_t launch_unpack8_step(const spa2_pack8_tensor (&t)[2], const ColumnOrder& order, cudaStream_t s) {
+  Pack8Args a{};
+  std::copy(t, t + 2, a.t);
+  a.n = 2;
+  a.order = order;
+  const long long places = t[0].rows * t[0].d / CHUNK;  // whole groups: d is 64 or 128
+  KernelTimer kt(KID_UNPACK8, s);
+  unpack8_kernel<__nv_bfloat16, true, true><<<dim3((unsigned)((places + PLACES - 1) / PLACES), 3), THREADS, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 static spa2_status pack8_call(const spa2_pack8_tensor* t, int n, int dtype, bool unpack, spa2_stream_t stream) {
@@ -265,8 +279,9 @@ static spa2_status pack8_call(const spa2_pack8_tensor* t, int n, int dtype, bool
     if (t[i].rows && (!t[i].x || !t[i].codes || !t[i].exps || reinterpret_cast<uintptr_t>(t[i].x) % esz))
       return SPA2_ERR_INVALID_ARG;
   }
-  return launch_pack8(t, n, dtype, unpack, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SPA2_OK
-                                                                                                 : SPA2_ERR_CUDA;
+  Pack8Args a{};
+  std::copy(t, t + n, a.t);
+  return launch(a, n, dtype, unpack, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SPA2_OK : SPA2_ERR_CUDA;
 }
 
 }  // namespace spa2
