@@ -44,14 +44,14 @@ class Packed:
     def empty_like(cls, x: torch.Tensor) -> "Packed":
         shape = x.shape
         _, at, groups = cls._sizes(shape)
-        return cls(torch.empty(at + groups, dtype=torch.uint8, device=x.device), shape, x.dtype)
+        return cls(x.new_empty(at + groups, dtype=torch.uint8), shape, x.dtype)
 
     @classmethod
     def several_like(cls, x: torch.Tensor, n: int) -> tuple:
         """n checkpoints of tensors like x in one buffer."""
         _, at, groups = cls._sizes(x.shape)
         size = n * ((at + groups + 15) & ~15)
-        return cls.several_in(torch.empty(size, dtype=torch.uint8, device=x.device), x.shape, x.dtype, n)
+        return cls.several_in(x.new_empty(size, dtype=torch.uint8), x.shape, x.dtype, n)
 
     @classmethod
     def several_in(cls, base, shape, dtype, n) -> tuple:
@@ -132,6 +132,6 @@ def unpack8(*packed: Packed) -> tuple[torch.Tensor, ...]:
     for p in packed:
         if p.base.device != device or device.type != "cuda":
             raise ValueError("unpack8 expects checkpoints on one CUDA device")
-    items = [(p, torch.empty(p.shape, dtype=dtype, device=device)) for p in packed]
+    items = [(p, p.base.new_empty(p.shape, dtype=dtype)) for p in packed]
     _launch(b.lib().spa2_unpack8, items, dtype, device, "spa2_unpack8")
     return tuple([x for _, x in items])

@@ -157,7 +157,7 @@ def _turned(spec, inverse: bool, strides, xs):
         if x.stride(3) != 1 and d != 1:
             x = x.contiguous()
             keep.append(x)
-        y = torch.empty(shape, dtype=dtype, device=device) if st is None else \
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if st is None else \
             torch.empty_strided(shape, st, dtype=dtype, device=device)
         outs.append(y)
         if B and shape[1] and N:
