@@ -248,10 +248,11 @@ def test_only_8_bits_are_kept_and_a_second_backward_is_refused():
     m = block_mask(q.detach(), k.detach(), 0.2, 0.6)
     sparse_attention(q, k, v, mask=m, checkpoint="int8").sum().backward()   # workspaces exist from here on
     torch.cuda.synchronize()
-    before = torch.cuda.memory_allocated()
+    requested = lambda: torch.cuda.memory_stats()["requested_bytes.all.current"]  # noqa: E731  (not the allocator's blocks)
+    before = requested()
     o = sparse_attention(q, k, v, mask=m, checkpoint="int8")
     torch.cuda.synchronize()
-    kept_bytes = torch.cuda.memory_allocated() - before - o.numel() * 2
+    kept_bytes = requested() - before - o.numel() * 2
     assert kept_bytes <= 3 * 33 / 32 * q.numel() + 16384
     loss = o.float().sum()
     loss.backward()
@@ -337,6 +338,70 @@ def test_bad_masks_are_reported():
             pass
     attention(q, k, v, dout, good)
     check_errors()
+
+
+def lists(keep):
+    """The mask of a dense bool [B, H, T_m, T_n]."""
+    def csr(x):
+        n = x.shape[-1]
+        ids = torch.where(x, torch.arange(n), n).sort(dim=-1).values.clamp(max=n - 1)
+        return x.sum(-1).int().contiguous().cuda(), ids.int().contiguous().cuda()
+
+    return b.Mask(*csr(keep), *csr(keep.transpose(-1, -2)))
+
+
+@pytest.mark.parametrize("N,d,bq,bkv", [(1100, 128, 128, 64), (1100, 64, 128, 64), (1100, 64, 64, 64), (1030, 128, 256, 128)])
+def test_every_count_of_kept_blocks(N, d, bq, bkv):
+    """Row i keeps i + 1 blocks, then all of them: one tile, two, .. and the columns that nobody keeps."""
+    q, k, v = synth.gaussian_with_sinks(B=1, H=2, N=N, d=d, seed=N + bq, device="cuda")
+    dout = synth.normal_like(q.shape, seed=N, device="cuda")
+    Tm, Tn = b.block_counts(N, bq, bkv)
+    keep = torch.zeros(1, 2, Tm, Tn, dtype=torch.bool)
+    for i in range(Tm):
+        keep[0, 0, i, :min(i + 1, Tn)] = True
+        keep[0, 1, i, Tn - 1 - i % Tn] = True          # one block each; from the ragged last one on
+        keep[0, 1, i, :i // 2] = True
+    against_oracle(q, k, v, dout, lists(keep), bq, bkv)
+
+
+def test_more_than_2_31_elements_in_the_attention():
+    """The last heads of a problem of more than 2^31 elements, against the same heads alone, bit for bit."""
+    H, N, d = 130, 131072, 128
+    Tm, Tn = b.block_counts(N)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v, dout = (torch.zeros(1, H, N, d, dtype=BF16, device="cuda") for _ in range(4))
+    for x in (q, k, v, dout):
+        x[0, -2:] = torch.randn(2, N, d, generator=g, device="cuda").to(BF16)
+    i, j = torch.arange(Tm, device="cuda", dtype=torch.int32), torch.arange(Tn, device="cuda", dtype=torch.int32)
+
+    def mask(H):   # query block i keeps the two key blocks of its own rows
+        m = b.Mask(torch.full((1, H, Tm), 2, dtype=torch.int32, device="cuda"),
+                   torch.zeros(1, H, Tm, Tn, dtype=torch.int32, device="cuda"),
+                   torch.ones(1, H, Tn, dtype=torch.int32, device="cuda"),
+                   torch.zeros(1, H, Tn, Tm, dtype=torch.int32, device="cuda"))
+        m.row_idx[..., 0], m.row_idx[..., 1], m.col_idx[..., 0] = 2 * i, 2 * i + 1, j // 2
+        return m
+
+    got = attention(q, k, v, dout, mask(H))
+    want = attention(*(x[:, -2:].contiguous() for x in (q, k, v, dout)), mask(2))
+    check_errors()
+    assert all(torch.equal(a[:, -2:], w) for a, w in zip(got, want))
+    assert all(w.float().abs().sum() > 0 for w in want) and not any(a[:, :-2].any() for a in got[1:])
+
+
+def test_checkpoints_moved_to_the_host_and_back():
+    """Saved tensors that come back at other addresses."""
+    q, k, v = synth.gaussian_with_sinks(B=1, H=2, N=500, d=64, seed=15, device="cuda")
+    dout = synth.normal_like(q.shape, seed=16, device="cuda")
+    inv_freq, axes = axial_frequencies(64, device="cuda")
+    r = Rotary(inv_freq, grid_positions(5, 10, 10, device="cuda"), axes=axes)
+    m = block_mask(q, k, 0.3, 0.6)
+    want = attention(q, k, v, dout, m, rotary=r)
+    with torch.autograd.graph.save_on_cpu():
+        leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+        o = sparse_attention(*leaves, mask=m, checkpoint="int8", rotary=r)
+    got = torch.autograd.grad(o, leaves, dout)
+    assert torch.equal(o, want[0]) and all(torch.equal(a, c) for a, c in zip(got, want[1:]))
 
 
 def test_fp32_gradients_through_the_binding():

@@ -142,6 +142,34 @@ def test_packed_layout():
     assert e.codes.shape == (0, 4) and e.exponents.shape == (0, 1) and e.nbytes == 0
 
 
+def test_several_checkpoints_in_one_buffer():
+    x = torch.zeros(3, 33, dtype=torch.bfloat16)      # 99 codes, 112 with the padding, and 6 exponents
+    kept = checkpoint.Packed.several_like(x, 3)
+    assert kept[0].base.numel() == 3 * 128 and [p.offset for p in kept] == [0, 128, 256]
+    for p in kept:
+        assert p.nbytes == 118 and p.data.numel() == 118 and p.codes.shape == (3, 33) and p.exponents.shape == (3, 2)
+        assert p.codes.data_ptr() == p.base.data_ptr() + p.offset and p.fields()[1:3] == (
+            p.codes.data_ptr(), p.exponents.data_ptr())
+    again = checkpoint.Packed.several_in(kept[0].base, x.shape, x.dtype, 3)
+    assert [p.fields() for p in again] == [p.fields() for p in kept]
+
+
+def test_status_fetch_argument_errors(L):
+    assert L.spa2_status_fetch(None, FAKE, None) == b.ERR_WORKSPACE
+    assert L.spa2_status_fetch(FAKE, None, None) == L.spa2_status_fetch(FAKE, FAKE + 2, None) == b.ERR_INVALID_ARG
+
+
+def test_packed_rotary_spec_points_at_its_tensors():
+    f, pos = torch.ones(4, dtype=torch.float64), torch.arange(5)
+    spec, _ = rotary._spec(rotary.Rotary(f, pos), 2, 5, 8, torch.device("cpu"))
+    assert b.rotary_spec_points(spec, f, pos)
+    assert not b.rotary_spec_points(spec, f.clone(), pos) and not b.rotary_spec_points(spec, f, pos.clone())
+    assert not b.rotary_spec_points(spec, f, None)
+    every_other = torch.ones(8, dtype=torch.float64)[::2]      # copied for the call: not to be kept
+    spec, copy = rotary._spec(rotary.Rotary(every_other, pos), 2, 5, 8, torch.device("cpu"))
+    assert copy.is_contiguous() and not b.rotary_spec_points(spec, every_other, pos)
+
+
 def test_sparse_attention_checkpoint_refusals():
     q = torch.zeros(1, 2, 128, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):

@@ -19,8 +19,8 @@ pinned host memory; the next call on that shape and stream raises `Spa2Error`
 once such a copy has landed with an error in it, and `check_errors()` waits for
 every pending copy and raises.
 
-Workspaces are cached per (shape, device, CUDA stream): calls on different
-streams never share scratch memory. A call that is captured into a CUDA graph gets
+Workspaces are cached per (shape, device, CUDA stream) and allocated when an
+operation first needs one: calls on different streams never share scratch memory. A call that is captured into a CUDA graph gets
 workspaces of its own, from the graph's memory, and its device-side errors are not
 reported (a replay reads no status word).
 
@@ -108,14 +108,14 @@ class _NoWatch:
 def _spa(B, H, N, d, device, bq=b.BQ, bkv=b.BKV) -> b.Spa2:
     if torch.cuda.is_current_stream_capturing():
         # graphs replay on any stream, two of them at once: each call owns its workspaces
-        s = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv)
+        s = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv, lazy=True)
         s.watch = _NoWatch()
         return s
     index = torch.cuda.current_device() if device.index is None else device.index
     key = (B, H, N, d, bq, bkv, index, torch._C._cuda_getCurrentRawStream(index))
     s = _cache.get(key)
     if s is None:
-        s = _cache[key] = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv)
+        s = _cache[key] = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv, lazy=True)
         s.watch = _StatusWatch(s)
     s.watch.poll()
     return s
@@ -223,9 +223,10 @@ def block_mask(q, k, k_frac: float, p_frac: float, bq: int = b.BQ, bkv: int = b.
         raise TypeError("block_mask expects bf16 q, k")
     q, k = q.contiguous(), k.contiguous()
     B, H, N, d = q.shape
-    s = _spa(B, H, N, d, q.device, bq, bkv)
-    m = s.block_mask(q, k, k_frac, p_frac)
-    s.watch.after([b.OP_MASK])
+    with b.on_device(q.device):
+        s = _spa(B, H, N, d, q.device, bq, bkv)
+        m = s.block_mask(q, k, k_frac, p_frac)
+        s.watch.after([b.OP_MASK])
     return m
 
 

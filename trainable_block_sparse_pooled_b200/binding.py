@@ -324,14 +324,31 @@ def on_device(device):
     return torch.cuda.device(device)
 
 
+class _Workspaces(dict):
+    """op -> workspace of one Spa2, allocated at the op's first use. Only the status words
+    are cleared (an op never run reads as OK); kernels write the rest before they read it."""
+
+    def __init__(self, spa: "Spa2"):
+        self.spa = spa
+
+    def __missing__(self, op):
+        s = self.spa
+        n = lib().spa2_workspace_bytes(op, s.B, s.H, s.N, s.d, s.bq, s.bkv)
+        ws = self[op] = s.torch.empty(n, dtype=s.torch.uint8, device=s.device)
+        ws[:256].zero_()
+        return ws
+
+
 class Spa2:
     """Torch-tensor front end of the C ABI for one problem shape.
 
     Buffers (mask, workspaces, outputs) are allocated through torch by the
-    caller side of the ABI; the library itself never allocates.
+    caller side of the ABI; the library itself never allocates. The workspaces of
+    the mask, the forward and the backward exist from the start unless `lazy`;
+    that of bwd_ckpt is allocated at its first call.
     """
 
-    def __init__(self, B, H, N, d, device="cuda", with_pbar=False, with_bitmap=False, bq=BQ, bkv=BKV):
+    def __init__(self, B, H, N, d, device="cuda", with_pbar=False, with_bitmap=False, bq=BQ, bkv=BKV, lazy=False):
         import torch
         self.torch = torch
         self.B, self.H, self.N, self.d = B, H, N, d
@@ -342,8 +359,10 @@ class Spa2:
         self.ws_bytes = {op: L.spa2_workspace_bytes(op, B, H, N, d, bq, bkv) for op in (OP_MASK, OP_FWD, OP_BWD)}
         if min(self.ws_bytes.values()) == 0:
             raise Spa2Error(ERR_UNSUPPORTED, f"shape B={B} H={H} N={N} d={d} bq={bq} bkv={bkv}")
-        # zero-filled so that the status word of an op never run reads as OK
-        self.ws = {op: torch.zeros(n, dtype=torch.uint8, device=device) for op, n in self.ws_bytes.items()}
+        self.ws = _Workspaces(self)
+        if not lazy:
+            # zero-filled so that the status word of an op never run reads as OK
+            self.ws.update((op, torch.zeros(n, dtype=torch.uint8, device=device)) for op, n in self.ws_bytes.items())
         self.with_pbar, self.with_bitmap = with_pbar, with_bitmap
 
     def new_mask(self) -> Mask:
@@ -397,14 +416,6 @@ class Spa2:
                                     _stream(t)), "spa2_sparse_attn_bwd")
         return dq, dk, dv
 
-    def _ckpt_ws(self):
-        """The workspace of bwd_ckpt, allocated at its first call (it holds the kept values in bf16)."""
-        ws = self.ws.get(OP_BWD_CKPT)
-        if ws is None:
-            n = lib().spa2_workspace_bytes(OP_BWD_CKPT, self.B, self.H, self.N, self.d, self.bq, self.bkv)
-            ws = self.ws[OP_BWD_CKPT] = self.torch.zeros(n, dtype=self.torch.uint8, device=self.device)
-        return ws
-
     def fwd_ckpt(self, q, k, v, mask: Mask, scale=0.0, lse=None):
         """O (bf16) and the 8-bit checkpoints of q, k, v (checkpoint.Packed), all that bwd_ckpt needs."""
         from .checkpoint import Packed
@@ -425,7 +436,7 @@ class Spa2:
         gt = t.float32 if grad_dtype == DTYPE_F32 else t.bfloat16
         dq, dk, dv = (t.empty_like(dout, dtype=gt) for _ in range(3))
         cm = mask.c()
-        ws = self._ckpt_ws()
+        ws = self.ws[OP_BWD_CKPT]
         _check(spa2_sparse_attn_bwd_ckpt(*(p.c() for p in kept), dout.data_ptr(), self.B, self.H, self.N, self.d,
                                          self.bq, self.bkv, cm, float(scale), dq.data_ptr(), dk.data_ptr(),
                                          dv.data_ptr(), int(grad_dtype), ws.data_ptr(), ws.numel(), _stream(t)),

@@ -132,6 +132,8 @@ def unpack8(*packed: Packed) -> tuple[torch.Tensor, ...]:
     for p in packed:
         if p.base.device != device or device.type != "cuda":
             raise ValueError("unpack8 expects checkpoints on one CUDA device")
+        if p.base.dtype != torch.uint8 or not p.base.is_contiguous() or p.base.numel() - p.offset < p.nbytes:
+            raise ValueError("unpack8 expects checkpoints as pack8 makes them")
     items = [(p, p.base.new_empty(p.shape, dtype=dtype)) for p in packed]
     _launch(b.lib().spa2_unpack8, items, dtype, device, "spa2_unpack8")
     return tuple([x for _, x in items])
