@@ -90,6 +90,23 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   const int bh = blockIdx.y;
   const long long rowid = (long long)bh * Tm + i;
 
+  // what the start waits for, asked for at once: the row's count and first block, and (warps
+  // 0-7) Q_i's codes, 16 elements of a row at a time, neighbours in neighbouring threads
+  constexpr int PER_ROW = D / 16, PIECES = 128 * PER_ROW / 256;
+  const int count = row_cnt[rowid], first = row_idx[rowid * Tn];
+  uint4 code[PIECES];
+  uint8_t E[PIECES];
+  if (warp < 8) {
+#pragma unroll
+    for (int x = 0; x < PIECES; ++x) {
+      const int piece = x * 256 + threadIdx.x, pr = piece / PER_ROW, c = piece % PER_ROW;
+      const long long at = (long long)bh * N + (long long)i * 128 + pr;
+      const bool there = i * 128 + pr < N;
+      code[x] = there ? reinterpret_cast<const uint4*>(q8 + at * D)[c] : make_uint4(0, 0, 0, 0);
+      E[x] = there ? qe[at * (D / 32) + (c >> 1)] : (uint8_t)0;
+    }
+  }
+
   if (warp == 9) {
     tmem_alloc(&sm.tmem_base, 256);
     tmem_relinquish();
@@ -119,7 +136,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   const WaitCtx wc{&sm.abort_flag, status, wait_limit_ns};
   const WaitCtx drain_wc{&sm.never, nullptr, wait_limit_ns};
 
-  int n = __shfl_sync(0xffffffffu, row_cnt[rowid], 0);  // warp-uniform
+  int n = __shfl_sync(0xffffffffu, count, 0);  // warp-uniform
   if (n < 1 || n > Tn) {
     if (threadIdx.x == 0) report(status, SPA2_ERR_DEVICE_BOUNDS);
     n = 0;
@@ -140,7 +157,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       while (vt < end) {
         // K(kt) needs the products of K(kt - 2) done, V(vt) dP(vt - 1); whichever is free
         if (kt < end && (kt < 2 || mbar_test_wait(&sm.k_empty[kt & 1], ((kt >> 1) - 1) & 1))) {
-          const int j = kv_list[kt < n ? kt : kt - n] & TILE_ID_MASK;
+          const int j = (kt == 0 ? first : kv_list[kt < n ? kt : kt - n]) & TILE_ID_MASK;
           if (j >= Tn) {
             report(status, SPA2_ERR_DEVICE_BOUNDS);
             sm.abort_flag = 1;
@@ -154,7 +171,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
           }
           ++kt;
         } else if (vt < kt && (vt < 1 || mbar_test_wait(&sm.v_empty, (vt - 1) & 1))) {
-          const int j = kv_list[vt < n ? vt : vt - n] & TILE_ID_MASK;
+          const int j = (vt == 0 ? first : kv_list[vt < n ? vt : vt - n]) & TILE_ID_MASK;
           mbar_expect_tx(&sm.v_full, KV_BYTES);
           for (int c = 0; c < CH; ++c) tma_load_3d(sm.v[c], &tm_v, &sm.v_full, c * 64, j * 64, bh);
           ++vt;
@@ -258,20 +275,9 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const long long row = (long long)i * 128 + r;
     const bool rvalid = row < N;
-    // Q_i from its codes: 16 elements of a row at a time, neighbours in neighbouring threads
+    // Q_i from its codes into shared memory, and its fp16 copy
     {
-      constexpr int PER_ROW = D / 16, PIECES = 128 * PER_ROW / 256;
       bool bad = false;
-      uint4 code[PIECES];
-      uint8_t E[PIECES];
-#pragma unroll
-      for (int x = 0; x < PIECES; ++x) {
-        const int piece = x * 256 + threadIdx.x, pr = piece / PER_ROW, c = piece % PER_ROW;
-        const long long at = (long long)bh * N + (long long)i * 128 + pr;
-        const bool there = i * 128 + pr < N;
-        code[x] = there ? reinterpret_cast<const uint4*>(q8 + at * D)[c] : make_uint4(0, 0, 0, 0);
-        E[x] = there ? qe[at * (D / 32) + (c >> 1)] : (uint8_t)0;
-      }
 #pragma unroll
       for (int x = 0; x < PIECES; ++x) {
         const int piece = x * 256 + threadIdx.x, pr = piece / PER_ROW, c = piece % PER_ROW;
