@@ -330,8 +330,12 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
  * element of q instead of the 10 of q, k, v, o and o_lo in bf16).
  * spa2_sparse_attn_bwd_ckpt reads the checkpoints, finds the LSE of their values
  * and D = rowsum(dO * O) = sum_j P_ij dP_ij again (O itself is not computed) and
- * writes dQ, dK, dV: the gradients of the attention at the kept values, with the
- * arithmetic of spa2_sparse_attn_bwd.
+ * writes dQ, dK, dV: the gradients of the attention at the kept values. Products
+ * take fp16 operands and add up in fp32: the kept values (exact where a group's
+ * largest magnitude is between 4e-6 and 65504; beyond, clamped and reported as
+ * SPA2_ERR_RANGE), P and dS (11 bits each), and dO times a power of two per head
+ * that brings the head's largest |dO| into [4, 8), so that gradients of any size
+ * keep their precision (infinities and NaN are reported as SPA2_ERR_RANGE).
  * Keeping O and LSE instead of recomputing them is cheaper but not close: with q,
  * k, v rounded to 8 bits and O, LSE not, the rows of dS no longer sum to zero,
  * and sink keys of 8x norm amplify that to 12% of dQ (4% with recomputation).

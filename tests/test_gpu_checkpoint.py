@@ -307,7 +307,7 @@ def test_values_beyond_fp16_are_reported():
     dout = synth.normal_like(q.shape, seed=7, device="cuda")
     m = block_mask(q, k, 1.0, 1.0)
     check_errors()
-    for at in range(4):
+    for at in range(3):   # not dout: it is scaled
         args = [q.clone(), k.clone(), v.clone(), dout.clone()]
         args[at][0, 0, 3, 3] = 1e6
         with pytest.raises(b.Spa2Error) as e:   # by the backward pass if the copy has landed, else by check_errors
@@ -316,6 +316,56 @@ def test_values_beyond_fp16_are_reported():
         assert e.value.code == b.ERR_RANGE
     attention(q, k, v, dout, m)
     check_errors()
+
+
+def test_gradients_scale_with_dout():
+    """Gradients are linear in dout: powers of two per head come through bit for bit, from gradients
+    of 1e-9 to ones of 1e6 (bf16 has the range; a half would not)."""
+    q, k, v = synth.gaussian_with_sinks(B=2, H=3, N=700, d=64, seed=17, device="cuda")
+    dout = synth.normal_like(q.shape, seed=18, device="cuda")
+    m = block_mask(q, k, 0.3, 0.6)
+    want = attention(q, k, v, dout, m)[1:]
+    powers = torch.tensor([[0, -30, 20], [-12, 7, -60]], device="cuda")[..., None, None]
+    got = attention(q, k, v, torch.ldexp(dout.float(), powers).to(BF16), m)[1:]
+    check_errors()
+    for a, w in zip(got, want):
+        assert torch.equal(a, torch.ldexp(w.float(), powers).to(BF16))
+    zero = attention(q, k, v, torch.zeros_like(dout), m)[1:]
+    assert not any(x.any() for x in zero)
+
+
+def test_small_rows_beside_large_ones():
+    """Rows of dout at 2^-12 of the others: what they alone contribute, the values' gradients of a key
+    block that only they keep. With the head's largest |dout| in [4, 8) (here it is: no scaling)
+    their fp16 elements are exact from 2^-17 up and off by at most 2^-25 below; over the 128 rows,
+    with P <= 1, that adds up to 2^-18. Both results are rounded to bf16, 2^-9 each of the value
+    (half a step is 2^-8 of a power of two, 2^-9 to 2^-8 relative)."""
+    q, k, v = synth.gaussian_with_sinks(B=1, H=1, N=512, d=64, seed=19, device="cuda")
+    dout = synth.normal_like(q.shape, seed=20, device="cuda")
+    small = dout.clone()
+    small[0, 0, 256:384] *= 2.0 ** -12
+    keep = torch.ones(1, 1, 4, 8, dtype=torch.bool)
+    keep[..., 5] = False
+    keep[0, 0, 2] = False
+    keep[0, 0, 2, 5] = True            # the third query block keeps the sixth key block, which nobody else does
+    m = lists(keep)
+    assert 4 <= small.abs().max() < 8
+    dv, dv_small = (attention(q, k, v, x, m)[3][0, 0, 320:384].double() for x in (dout, small))
+    assert ((dv_small - dv * 2.0 ** -12).abs() <= 2.0 ** -18 + 2 * 2.0 ** -8 * dv.abs() * 2.0 ** -12).all()
+    assert dv.abs().median() > 0.1   # 2.4e-5 of the small rows: six times what the sum allows
+
+
+def test_infinite_gradients_are_reported():
+    q, k, v = synth.gaussian_with_sinks(B=1, H=2, N=256, d=64, seed=21, device="cuda")
+    m = block_mask(q, k, 1.0, 1.0)
+    for bad in (math.inf, math.nan):
+        dout = synth.normal_like(q.shape, seed=22, device="cuda")
+        dout[0, 1, 100, 3] = bad
+        check_errors()
+        with pytest.raises(b.Spa2Error) as e:
+            attention(q, k, v, dout, m)
+            check_errors()
+        assert e.value.code == b.ERR_RANGE
 
 
 def test_bad_masks_are_reported():

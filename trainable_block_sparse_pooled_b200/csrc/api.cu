@@ -148,11 +148,13 @@ static BwdWs bwd_ws(void* ws, const Shape& s) {
 }
 
 // the backward on 8-bit checkpoints: the backward's own workspace, then the LSE that the dQ
-// pass finds and the kept values of k and v
+// pass finds, the kept values of k and v, and what scales dO
 struct CkptWs {
   BwdWs b;
   float* lse;
-  void *k, *v;  // [BH, N, d] bf16
+  void *k16, *v16;    // [BH, N, d] fp16
+  uint32_t* do_most;  // [BH, DO_PARTS]
+  float* unscale;     // [BH]
   size_t bytes;
 };
 static CkptWs ckpt_ws(void* ws, const Shape& s) {
@@ -162,10 +164,14 @@ static CkptWs ckpt_ws(void* ws, const Shape& s) {
   size_t off = w.b.bytes;
   w.lse = reinterpret_cast<float*>(base + off);
   off += al256((size_t)s.BH * s.N * 4);
-  for (void** p : {&w.k, &w.v}) {
+  for (void** p : {&w.k16, &w.v16}) {
     *p = base + off;
     off += al256((size_t)s.BH * s.N * s.d * 2);
   }
+  w.do_most = reinterpret_cast<uint32_t*>(base + off);
+  off += al256((size_t)s.BH * DO_PARTS * 4);
+  w.unscale = reinterpret_cast<float*>(base + off);
+  off += al256((size_t)s.BH * 4);
   w.bytes = off;
   return w;
 }
@@ -524,7 +530,8 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = grad_dtype == SPA2_DTYPE_F32;
   CUtensorMap tk, tv, tdo, tdob, tq16, tdq;
-  if (!make_map(&tk, w.k, s, 64) || !make_map(&tv, w.v, s, 64) || !make_map(&tdo, w.b.do16, s, 128, true) ||
+  if (!make_map(&tk, w.k16, s, 64, true) || !make_map(&tv, w.v16, s, 64, true) ||
+      !make_map(&tdo, w.b.do16, s, 128, true) ||
       !make_map(&tdob, dout, s, 128) || !make_map(&tq16, w.b.q16, s, 128, true) ||
       !(f32 ? make_map_f32(&tdq, dq, s, 128) : make_map(&tdq, dq, s, 128)))
     return SPA2_ERR_CUDA;
@@ -540,13 +547,13 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
     cc = t.csc_cnt;
     ci = t.csc_idx;
   }
-  const long long rows = s.BH * s.N;
-  const spa2_pack8_tensor t[2] = {{w.k, k8->codes, k8->exps, rows, d}, {w.v, v8->codes, v8->exps, rows, d}};
-  SPA2_CUDA_TRY(launch_unpack8_step(t, ColumnOrder{cc, (int)s.BH, s.TNt, w.b.col_order}, st));
-  BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, w.k, nullptr, nullptr, dout, w.v, w.lse, rc, ri, cc, ci,
+  SPA2_CUDA_TRY(launch_unpack8_step(Unpack8Step{*k8, *v8, static_cast<uint32_t*>(w.k16), static_cast<uint32_t*>(w.v16),
+                                                dout, w.do_most, cc, w.b.col_order, s.TNt, s.BH, (long long)s.N * d},
+                                    st));
+  BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, nullptr, nullptr, nullptr, dout, nullptr, w.lse, rc, ri, cc, ci,
             w.b.dvec, w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
             scale * 1.4426950408889634f, status, status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.b.col_order,
-            q8->codes, q8->exps, &tdob};
+            q8->codes, q8->exps, k8->exps, v8->exps, &tdob, w.do_most, w.unscale};
   SPA2_CUDA_TRY(launch_bwd(a, d, st));
   return SPA2_OK;
 }

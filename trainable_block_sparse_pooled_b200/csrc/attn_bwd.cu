@@ -104,7 +104,10 @@ SPA2_DEV void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
 // go on with the next column; a set's first dV/dK waits (acc_free) until its
 // gradients of two columns back have been read out. The next K_j / V_j is
 // loaded as soon as the last S / dP of the current column has run.
-template <int D, bool TILED>
+// KV16 (the backward on 8-bit checkpoints): K and V arrive as fp16, values beyond its range
+// clamped, which their groups' exponents tell (ke, ve); the gradients are multiplied by their
+// head's unscale (a power of two by which dO and D were divided).
+template <int D, bool TILED, bool KV16>
 __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q16,
                                                                   const __grid_constant__ CUtensorMap tm_k,
                                                                   const __grid_constant__ CUtensorMap tm_v,
@@ -114,6 +117,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_c
                                                                   const int* __restrict__ col_cnt,
                                                                   const int* __restrict__ col_idx,
                                                                   const int* __restrict__ col_order,
+                                                                  const float* __restrict__ unscale,
+                                                                  const uint8_t* __restrict__ ke,
+                                                                  const uint8_t* __restrict__ ve,
                                                                   void* __restrict__ dk, void* __restrict__ dv,
                                                                   int grad_f32, int N, int Tm, int Tn, int total_cols,
                                                                   int* __restrict__ ticket, float scale,
@@ -410,6 +416,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_c
       }
       if (n < 0 || !ok) return;
       tc_fence_after();
+      const float back = KV16 ? unscale[bh] : 1.f;
 #pragma unroll 1
       for (int which = 0; which < 2; ++which) {  // 0: dV, 1: dK
         uint32_t a[32], b[32];
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_c
         tmem_ld32(tl + col, a);
         tmem_ld32(tl + col + 32, b);
         tmem_wait_ld();
-        const float f = which == 0 ? 1.f : scale;
+        const float f = KV16 ? (which == 0 ? back : scale * back) : which == 0 ? 1.f : scale;
         void* dst = which == 0 ? dv : dk;
         if (r < D) {
           if (grad_f32) {
@@ -442,7 +449,14 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_c
       if (!wait_warp(&sm.kv_full, c & 1, wc)) ok = false;
       const int n = ok ? sm.col_n[c & 1] : END;
       const int j = sm.col_j[c & 1], bh = sm.col_bh[c & 1];
-      if (n > 0) {
+      if (KV16 && n > 0) {
+        const long long group = ((long long)bh * N + (long long)j * 64) * (D / 32);
+        bool bad = false;
+        for (int x = (int)threadIdx.x - 320; x < min(64, N - j * 64) * (D / 32); x += 128)
+          bad = bad || ke[group + x] > 142 || ve[group + x] > 142;  // a magnitude of 2^16 or more
+        if (bad) report(status, SPA2_ERR_RANGE);
+      }
+      if (!KV16 && n > 0) {
         // K_j, V_j (bf16, swizzled as loaded) -> fp16 in place, 16 bytes per step
         bool bad = false;
         constexpr int UNITS = CH * 64 * 128 / 16;  // 16-byte units of one tensor
@@ -954,10 +968,10 @@ static cudaError_t launch_pre(const BwdArgs& a, cudaStream_t s) {
 }
 
 // 2. dK, dV (kv-major)
-template <int D, bool TILED>
+template <int D, bool TILED, bool KV16>
 static cudaError_t launch_dkdv(const BwdArgs& a, cudaStream_t s) {
   const size_t smem = sizeof(BwdSmem<D>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(bwd_dkdv_kernel<D, TILED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(bwd_dkdv_kernel<D, TILED, KV16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
@@ -965,9 +979,9 @@ static cudaError_t launch_dkdv(const BwdArgs& a, cudaStream_t s) {
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int total_cols = a.BH * a.Tn;
   KernelTimer kt(KID_BWD_DKDV, s);
-  bwd_dkdv_kernel<D, TILED><<<dim3(std::min(total_cols, sms)), BWD_THREADS, smem, s>>>(
-      *a.tm_q16, *a.tm_k, *a.tm_v, *a.tm_do, a.lse, a.dvec, a.col_cnt, a.col_idx, a.col_order, a.dk, a.dv, a.grad_f32,
-      a.N, a.Tm, a.Tn, total_cols, a.ticket, a.scale, a.scale_log2, a.status, a.wait_limit_ns);
+  bwd_dkdv_kernel<D, TILED, KV16><<<dim3(std::min(total_cols, sms)), BWD_THREADS, smem, s>>>(
+      *a.tm_q16, *a.tm_k, *a.tm_v, *a.tm_do, a.lse, a.dvec, a.col_cnt, a.col_idx, a.col_order, a.unscale, a.ke, a.ve, a.dk, a.dv,
+      a.grad_f32, a.N, a.Tm, a.Tn, total_cols, a.ticket, a.scale, a.scale_log2, a.status, a.wait_limit_ns);
   return cudaGetLastError();
 }
 
@@ -991,10 +1005,10 @@ static cudaError_t launch_bwd_d(const BwdArgs& a, cudaStream_t s) {
   cudaError_t e;
   if (a.q8) {  // the dQ pass finds LSE and D and writes the fp16 copies, so it goes first
     if ((e = launch_dq_ckpt(a, D, s)) != cudaSuccess) return e;
-    return launch_dkdv<D, TILED>(a, s);
+    return launch_dkdv<D, TILED, true>(a, s);
   }
   if ((e = launch_pre<D>(a, s)) != cudaSuccess) return e;
-  if ((e = launch_dkdv<D, TILED>(a, s)) != cudaSuccess) return e;
+  if ((e = launch_dkdv<D, TILED, false>(a, s)) != cudaSuccess) return e;
   return launch_dq<D, TILED>(a, s);
 }
 

@@ -8,11 +8,18 @@
 //             a running maximum m, in fp32; then LSE = m + log2 l and D = w / l, for
 //             D = rowsum(dO * O) = sum_j P_ij dP_ij. The output O is never formed: no P V
 //             product, nothing of its size written or read.
-//     second  S and dP again, dS = P * (dP - D), dQ_i += dS K_j * scale, as in
-//             bwd_dq_kernel: dS as a hi + lo pair of bf16 values in tensor memory.
-//   Q_i is decoded from its codes into shared memory, dO_i, K_j and V_j (the kept values in
-//   bf16) arrive by TMA. The fp16 copies of Q and dO that the dK/dV pass streams are written
-//   from here as well (|x| > 65504 clamped and reported).
+//     second  S and dP again, dS = P * (dP - D), dQ_i += dS K_j * scale.
+//   Q_i is decoded from its codes into shared memory, dO_i, K_j and V_j arrive by TMA. The fp16
+//   copies of Q and dO that the dK/dV pass streams are written from here as well.
+//
+// Precision: every product takes fp16 operands and adds up in fp32, in this pass as in the dK/dV
+// pass. The kept values have 7 bits and are exact in fp16 (a group whose largest magnitude is
+// below 4e-6 loses up to 2^-25; above 65504 is clamped and reported). dO is multiplied by a power
+// of two per head that brings the head's largest |dO| into [4, 8) (gradients are linear in dO; the
+// loss's scale must not decide what is left of them), which leaves its 8 bits exact down to 2^-19 of
+// the largest. dS, formed in fp32, is rounded to 11 bits, as the dK/dV pass rounds it: relative to
+// dQ's norm 2e-4 in random rows and 8e-4 with sink keys of 8x norm, whose terms cancel, against
+// 1.65e-3 of bf16 gradients.
 //
 // What bounds it: each product chain of a CTA is serial (S and dP have one buffer each, dS
 // goes over S), so a second CTA on the SM works through its own chain meanwhile, and through
@@ -31,12 +38,12 @@ constexpr int DQC_THREADS = 320;  // S / dP / dS x 8 warps, TMA, MMA
 template <int D>
 struct DqcSmem {
   static constexpr int CH = D / 64;
-  // Q_i and dO_i bf16; at the end the staged dQ tile (64 KB in fp32 at d = 128)
+  // Q_i and dO_i fp16 (dO_i lands as bf16); at the end the staged dQ tile (64 KB in fp32 at d = 128)
   alignas(1024) uint8_t q[CH][128 * 128];
   alignas(1024) uint8_t dO[CH][128 * 128];
   alignas(1024) uint8_t k[2][CH][64 * 128];
   alignas(1024) uint8_t v[CH][64 * 128];
-  uint64_t q_ready, do_full;
+  uint64_t q_ready, do_full, do_ready;
   uint64_t k_full[2], k_empty[2], v_full, v_empty;
   uint64_t sdp_full, read, ds_full;  // S and dP there; read out; dS there
   uint64_t acc_done, drain;
@@ -51,28 +58,22 @@ SPA2_DEV bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
   return __all_sync(0xffffffff, ok);
 }
 
-SPA2_DEV void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(a, b);
-  const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi));
-  lo = pack_bf16(a - f.x, b - f.y);
-}
-
 }  // namespace
 
-// TMEM columns: S 0..63 (dS of kv columns 16c .. 16c+15 over it: hi 16c .. +7, lo 16c+8 .. +15),
+// TMEM columns: S 0..63 (dS of kv columns 32h .. 32h+31 over 32h .. 32h+15),
 // dP 64..127, dQ 128 .. 128+d (between the passes: what the two halves of a row exchange).
 template <int D, bool TILED>
 __global__ void __launch_bounds__(DQC_THREADS, 2)
     bwd_dq_ckpt_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
                        const int8_t* __restrict__ q8, const uint8_t* __restrict__ qe, uint4* __restrict__ q16,
-                       uint4* __restrict__ do16, float* __restrict__ lse,
-                       float* __restrict__ dvec, const int* __restrict__ row_cnt, const int* __restrict__ row_idx,
+                       uint4* __restrict__ do16, const uint32_t* __restrict__ do_most, float* __restrict__ unscale,
+                       float* __restrict__ lse, float* __restrict__ dvec, const int* __restrict__ row_cnt, const int* __restrict__ row_idx,
                        int grad_f32, int N, int Tm, int Tn, float scale, float scale_log2, int* status,
                        unsigned long long wait_limit_ns) {
   constexpr int CH = D / 64;
-  constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64, false, false);
-  constexpr uint32_t IDESC_Q = idesc_bf16_f32(128, D, false, true);
+  constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64, false, false, /*f16=*/true);
+  constexpr uint32_t IDESC_Q = idesc_bf16_f32(128, D, false, true, /*f16=*/true);
   constexpr uint32_t KV_BYTES = 64 * D * 2, ROW_BYTES = 128 * D * 2;
   constexpr uint32_t T_S = 0, T_DP = 64, T_DQ = 128;
   constexpr float LN2 = 0.69314718055994530942f;
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   // 0-7) Q_i's codes, 16 elements of a row at a time, neighbours in neighbouring threads
   constexpr int PER_ROW = D / 16, PIECES = 128 * PER_ROW / 256;
   const int count = row_cnt[rowid], first = row_idx[rowid * Tn];
+  const uint32_t most_part = do_most[(long long)bh * DO_PARTS + lane];
   uint4 code[PIECES];
   uint8_t E[PIECES];
   if (warp < 8) {
@@ -114,6 +116,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   if (threadIdx.x == 256) {
     mbar_init(&sm.q_ready, 256);
     mbar_init(&sm.do_full, 1);
+    mbar_init(&sm.do_ready, 256);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
@@ -220,17 +223,14 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
                     sdesc_sw128(smem_u32(sm.v[kk >> 2]) + (kk & 3) * 32, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
         mma_commit_el(&sm.v_empty);
       };
-      // dQ += dS(g) K(g), hi and lo, K = 64 kv rows
+      // dQ += dS(g) K(g), K = 64 kv rows
       auto issue_dq = [&](int g) {
         tc_fence_after();
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts_el(tmem + T_DQ, tmem + T_S + kk * 16 + part * 8,
-                      sdesc_sw128(smem_u32(sm.k[g & 1][0]) + kk * 2048, 64 * 128, 1024), IDESC_Q,
-                      (g > n || part > 0 || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_el(tmem + T_DQ, tmem + T_S + (kk >> 1) * 32 + (kk & 1) * 8,
+                    sdesc_sw128(smem_u32(sm.k[g & 1][0]) + kk * 2048, 64 * 128, 1024), IDESC_Q,
+                    (g > n || kk > 0) ? 1u : 0u);
         mma_commit_el(&sm.k_empty[g & 1]);
       };
       bool ok = wait_bar_all(&sm.q_ready, 0, wc);
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
         if (!ok) break;
         issue_s(g);
         if (g < n) mma_commit_el(&sm.k_empty[g & 1]);
-        ok = (g > 0 || wait_bar_all(&sm.do_full, 0, wc)) && wait_bar_all(&sm.v_full, g & 1, wc);
+        ok = (g > 0 || wait_bar_all(&sm.do_ready, 0, wc)) && wait_bar_all(&sm.v_full, g & 1, wc);
         if (!ok) break;
         issue_dp();
         mma_commit_el(&sm.sdp_full);
@@ -275,53 +275,58 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const long long row = (long long)i * 128 + r;
     const bool rvalid = row < N;
+    // the power of two that brings the head's largest |dO|, 2^(E - 127) or more, into [4, 8): its
+    // exponent field is 127 + 129 - E (for infinities and NaN, which are reported, and zeros any will do)
+    const uint32_t most_e = min(max(__reduce_max_sync(0xffffffffu, most_part) >> 23, 29u), 227u);
+    const float do_scale = __uint_as_float((256u - most_e) << 23);
+    const float back = __uint_as_float((most_e - 2u) << 23);  // its inverse
+    if (i == 0 && threadIdx.x == 0) unscale[bh] = back;
     // Q_i from its codes into shared memory, and its fp16 copy
-    {
-      bool bad = false;
+    bool bad = false;
 #pragma unroll
-      for (int x = 0; x < PIECES; ++x) {
-        const int piece = x * 256 + threadIdx.x, pr = piece / PER_ROW, c = piece % PER_ROW;
-        const float step = pack8_step(E[x]);
-        const uint32_t in[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
-        uint32_t w[8], w16[8];
+    for (int x = 0; x < PIECES; ++x) {
+      const int piece = x * 256 + threadIdx.x, pr = piece / PER_ROW, c = piece % PER_ROW;
+      const float step = pack8_step(E[x]);
+      const uint32_t in[4] = {code[x].x, code[x].y, code[x].z, code[x].w};
+      uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float f[4];
-          pack8_floats(in[e], f);
-          // codes of rows behind the last are 0, which the conversion takes for +0
-          w[2 * e] = pack_bf16(f[0] * step, f[1] * step);
-          w[2 * e + 1] = pack_bf16(f[2] * step, f[3] * step);
-          w16[2 * e] = pack_f16_clamped(f[0] * step, f[1] * step, bad);
-          w16[2 * e + 1] = pack_f16_clamped(f[2] * step, f[3] * step, bad);
-        }
-        if (i * 128 + pr < N) {
-          uint4* to = q16 + (((long long)bh * N + (long long)i * 128 + pr) * D + c * 16) / 8;
-          to[0] = make_uint4(w16[0], w16[1], w16[2], w16[3]);
-          to[1] = make_uint4(w16[4], w16[5], w16[6], w16[7]);
-        }
-        uint8_t* chunk = sm.q[c >> 2];
-        *reinterpret_cast<uint4*>(chunk + sw128_offset(pr, (c & 3) * 2)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(chunk + sw128_offset(pr, (c & 3) * 2 + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+      for (int e = 0; e < 4; ++e) {
+        float f[4];
+        pack8_floats(in[e], f);
+        // codes of rows behind the last are 0, which the conversion takes for +0
+        w[2 * e] = pack_f16_clamped(f[0] * step, f[1] * step, bad);
+        w[2 * e + 1] = pack_f16_clamped(f[2] * step, f[3] * step, bad);
+      }
+      const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+      uint8_t* chunk = sm.q[c >> 2];
+      *reinterpret_cast<uint4*>(chunk + sw128_offset(pr, (c & 3) * 2)) = lo;
+      *reinterpret_cast<uint4*>(chunk + sw128_offset(pr, (c & 3) * 2 + 1)) = hi;
+      if (i * 128 + pr < N) {
+        uint4* to = q16 + (((long long)bh * N + (long long)i * 128 + pr) * D + c * 16) / 8;
+        to[0] = lo;
+        to[1] = hi;
+      }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&sm.q_ready);
+    // dO_i to fp16 in place, 8 elements of a row at a time, and its copy
+    if (n > 0 && wait_warp(&sm.do_full, 0, wc)) {
+#pragma unroll
+      for (int x = 0; x < 128 * D / 8 / 256; ++x) {
+        const int piece = x * 256 + threadIdx.x, pr = piece / (D / 8), c = piece % (D / 8);
+        uint4* at = reinterpret_cast<uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7));
+        auto to16 = [&](uint32_t w) {
+          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+          return pack_f16_clamped(f.x * do_scale, f.y * do_scale, bad);
+        };
+        const uint4 in = *at, out = make_uint4(to16(in.x), to16(in.y), to16(in.z), to16(in.w));
+        *at = out;
+        if (i * 128 + pr < N) do16[(((long long)bh * N + (long long)i * 128 + pr) * D) / 8 + c] = out;
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sm.q_ready);
-      // fp16 copy of dO_i, 8 elements of a row at a time
-      if (n > 0 && wait_warp(&sm.do_full, 0, wc)) {
-#pragma unroll
-        for (int x = 0; x < 128 * D / 8 / 256; ++x) {
-          const int piece = x * 256 + threadIdx.x, pr = piece / (D / 8), c = piece % (D / 8);
-          if (i * 128 + pr >= N) continue;
-          const uint4 in = *reinterpret_cast<const uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7));
-          auto to16 = [&bad](uint32_t w) {
-            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-            return pack_f16_clamped(f.x, f.y, bad);
-          };
-          do16[(((long long)bh * N + (long long)i * 128 + pr) * D) / 8 + c] =
-              make_uint4(to16(in.x), to16(in.y), to16(in.z), to16(in.w));
-        }
-      }
-      if (bad) report(status, SPA2_ERR_RANGE);
+      mbar_arrive(&sm.do_ready);
     }
+    if (bad) report(status, SPA2_ERR_RANGE);
     const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
     // only kv-block Tn-1 (last in the ascending list) is ragged
     const int last_valid = (n > 0 && (kv_list[n - 1] & TILE_ID_MASK) == Tn - 1) ? N - (Tn - 1) * 64 : 64;
@@ -420,10 +425,11 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&sm.read);  // dP may be overwritten
+      uint32_t ds[16];
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
         const int c0 = h * 32 + sub * 16;
-        uint32_t sa[16], ds[16];  // dS: hi, lo
+        uint32_t sa[16];
         tmem_ld16(tl + T_S + c0, sa);
         tmem_wait_ld();
 #pragma unroll
@@ -440,21 +446,22 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
               f2_sub(f2_pack(__uint_as_float(pa[sub * 16 + 2 * e]), __uint_as_float(pa[sub * 16 + 2 * e + 1])), d2));
           float s0, s1;
           f2_unpack(ds2, s0, s1);
-          split_bf16(s0, s1, ds[e], ds[8 + e]);
+          ds[sub * 8 + e] = pack_f16(s0, s1);
         }
-        tmem_st16(tl + T_S + c0, ds);  // over these columns of S (read by this warp alone)
       }
+      tmem_st16(tl + T_S + h * 32, ds);  // over these columns of S (read by this warp alone)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sm.ds_full);
     }
-    // epilogue: dQ_i = scale * acc, warpgroup h holding feature columns h*D/2 .. +D/2, staged in
+    // epilogue: dQ_i = scale * acc without dO's factor, warpgroup h holding feature columns h*D/2 .. +D/2, staged in
     // the space of Q and dO (every product is done) as 128-byte-swizzled boxes of 128 rows x 128
     // bytes (32 fp32 or 64 bf16 columns) for the TMA stores below; the tensor map clips the rows
     // of a ragged last q-block
     if (ok) ok = wait_warp(&sm.acc_done, 0, wc);
     if (ok) {
       tc_fence_after();
+      const float f = scale * back;
       uint8_t* stage = &sm.q[0][0];
 #pragma unroll 1
       for (int cc = 0; cc < D / 64; ++cc) {
@@ -467,18 +474,18 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<float4*>(box + sw128_offset(r, e)) =
-                make_float4(__uint_as_float(a[4 * e]) * scale, __uint_as_float(a[4 * e + 1]) * scale,
-                            __uint_as_float(a[4 * e + 2]) * scale, __uint_as_float(a[4 * e + 3]) * scale);
+                make_float4(__uint_as_float(a[4 * e]) * f, __uint_as_float(a[4 * e + 1]) * f,
+                            __uint_as_float(a[4 * e + 2]) * f, __uint_as_float(a[4 * e + 3]) * f);
         } else {
           uint8_t* box = stage + (c0 / 64) * (128 * 128);
           const uint32_t u0 = (uint32_t)((c0 % 64) / 8);  // 16-byte unit of the slice in its 64-column box
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             *reinterpret_cast<uint4*>(box + sw128_offset(r, u0 + e)) =
-                make_uint4(pack_bf16(__uint_as_float(a[8 * e]) * scale, __uint_as_float(a[8 * e + 1]) * scale),
-                           pack_bf16(__uint_as_float(a[8 * e + 2]) * scale, __uint_as_float(a[8 * e + 3]) * scale),
-                           pack_bf16(__uint_as_float(a[8 * e + 4]) * scale, __uint_as_float(a[8 * e + 5]) * scale),
-                           pack_bf16(__uint_as_float(a[8 * e + 6]) * scale, __uint_as_float(a[8 * e + 7]) * scale));
+                make_uint4(pack_bf16(__uint_as_float(a[8 * e]) * f, __uint_as_float(a[8 * e + 1]) * f),
+                           pack_bf16(__uint_as_float(a[8 * e + 2]) * f, __uint_as_float(a[8 * e + 3]) * f),
+                           pack_bf16(__uint_as_float(a[8 * e + 4]) * f, __uint_as_float(a[8 * e + 5]) * f),
+                           pack_bf16(__uint_as_float(a[8 * e + 6]) * f, __uint_as_float(a[8 * e + 7]) * f));
         }
       }
       fence_proxy_async_smem();
@@ -510,8 +517,8 @@ static cudaError_t launch_dq_ckpt_t(const BwdArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   KernelTimer kt(KID_BWD_DQ_CKPT, s);
   bwd_dq_ckpt_kernel<D, TILED><<<dim3(a.Tm, a.BH), DQC_THREADS, smem, s>>>(
-      *a.tm_dob, *a.tm_k, *a.tm_v, *a.tm_dq, a.q8, a.qe, static_cast<uint4*>(a.q16), static_cast<uint4*>(a.do16), a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N, a.Tm, a.Tn,
-      a.scale, a.scale_log2, a.status, a.wait_limit_ns);
+      *a.tm_dob, *a.tm_k, *a.tm_v, *a.tm_dq, a.q8, a.qe, static_cast<uint4*>(a.q16), static_cast<uint4*>(a.do16), a.do_most, a.unscale, a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N,
+      a.Tm, a.Tn, a.scale, a.scale_log2, a.status, a.wait_limit_ns);
   return cudaGetLastError();
 }
 

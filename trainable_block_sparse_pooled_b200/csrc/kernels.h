@@ -119,11 +119,13 @@ struct BwdArgs {
   unsigned long long wait_limit_ns;
   int tiled;          // list entries may carry tile exclusion bits
   int* col_order;     // [BH * Tn]: the dK/dV pass's columns, head by head, long columns first (pre-pass)
-  // on 8-bit checkpoints (otherwise null): Q's codes and exponents; col_order is already there, k and
-  // v are the kept values, and the dQ pass writes lse, dvec, do16 and q16
+  // on 8-bit checkpoints (otherwise null): Q's codes and exponents; tm_k and tm_v are fp16, col_order
+  // and do_most are there, and the dQ pass writes lse, dvec, do16, q16 and unscale
   const int8_t* q8;
-  const uint8_t* qe;
+  const uint8_t *qe, *ke, *ve;
   const CUtensorMap* tm_dob;  // dO bf16, box {64, 128, 1}
+  const uint32_t* do_most;    // [BH, DO_PARTS]
+  float* unscale;             // [BH]: do16 and dvec are dO and D divided by this power of two
 };
 cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s);
 
@@ -133,13 +135,19 @@ cudaError_t launch_dq_ckpt(const BwdArgs& a, int d, cudaStream_t s);
 // pack8.cu. The checkpoints of a step's q, k, v [rows, d] bf16 (d = 64 or 128, 16-byte aligned),
 // with an fp16 copy of v; |v| > 65504 is clamped and reported to status
 cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* status, cudaStream_t s);
-// and the kept values of k, v, with the order in which the dK/dV pass takes its columns
-struct ColumnOrder {
-  const int* cnt;  // [heads, Tn] column counts
-  int heads, Tn;
-  int* out;        // BwdArgs::col_order
+// and what the backward starts from: k, v as fp16, the dK/dV pass's columns in order, the largest |dO|
+constexpr int DO_PARTS = 32;  // parts of a head whose largest |dO| are found apart
+struct Unpack8Step {
+  spa2_pack8_tensor k, v;
+  uint32_t *k16, *v16;
+  const void* dout;   // bf16, 16-byte aligned
+  uint32_t* do_most;  // [heads, DO_PARTS] fp32 bits
+  const int* col_cnt;
+  int* col_order;
+  int Tn;
+  long long heads, per_head;  // N * d elements to a head
 };
-cudaError_t launch_unpack8_step(const spa2_pack8_tensor (&t)[2], const ColumnOrder& order, cudaStream_t s);
+cudaError_t launch_unpack8_step(const Unpack8Step& a, cudaStream_t s);
 
 // api.cu
 cudaError_t launch_timeout_probe(int* status, unsigned long long limit_ns, cudaStream_t s);

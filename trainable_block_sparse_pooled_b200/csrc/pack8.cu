@@ -25,9 +25,6 @@ struct Pack8Args {
   int* status;                          // where |x| > 65504 is reported; needed for a copy
   uint32_t per_row[SPA2_PACK8_MAX];     // chunk places of a row, and x / per_row = x * div_mul >> (32 + div_shift)
   uint32_t div_mul[SPA2_PACK8_MAX], div_shift[SPA2_PACK8_MAX];  // for x < 2^31
-  // ORDER: the blocks beyond the n tensors write the order in which the dK/dV pass takes its columns
-  int n;
-  ColumnOrder order;
 };
 
 constexpr int CHUNK = 8, PER_GROUP = 4, UNROLL = 4, THREADS = 256;
@@ -91,8 +88,8 @@ SPA2_DEV uint32_t chunk_exponent(const Chunk<T>& x) {
   }
 }
 
-// fp16 copy of a chunk of a bf16 tensor; below 2^16 (E <= 142) bf16 values are at most 65280 and
-// no element needs a look
+// fp16 copy of a chunk of a bf16 tensor or of kept values, whose largest has the exponent E; below
+// 2^16 (E <= 142) these are at most 65280 and no element needs a look
 SPA2_DEV void store_f16(uint32_t* to, const float (&f)[CHUNK], uint32_t E, bool& bad) {
   uint4 w;
   if (E <= 142u)
@@ -148,13 +145,8 @@ __global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) pack8
   if (bad) report(a.status, SPA2_ERR_RANGE);
 }
 
-template <typename T, bool FLAT, bool ORDER>
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) unpack8_kernel(const __grid_constant__ Pack8Args a) {
-  if (ORDER && blockIdx.y == a.n) {
-    for (int head = blockIdx.x; head < a.order.heads; head += gridDim.x)
-      longest_first(a.order.cnt, a.order.Tn, head, a.order.out);
-    return;
-  }
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
   const Places<FLAT> places(a);
   long long e[UNROLL], group;
@@ -233,7 +225,7 @@ static cudaError_t launch_pack8_t(Pack8Args& a, int n, bool unpack, cudaStream_t
   KernelTimer kt(unpack ? KID_UNPACK8 : KID_PACK8, s);
   if (chunks) {
     const dim3 grid((unsigned)((groups * PER_GROUP + PLACES - 1) / PLACES), (unsigned)n);
-    auto* k = unpack ? (flat ? unpack8_kernel<T, true, false> : unpack8_kernel<T, false, false>)
+    auto* k = unpack ? (flat ? unpack8_kernel<T, true> : unpack8_kernel<T, false>)
                      : (flat ? pack8_kernel<T, true> : pack8_kernel<T, false>);
     k<<<grid, THREADS, 0, s>>>(a);
   } else {
@@ -257,14 +249,74 @@ cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* s
   return launch(a, 3, SPA2_DTYPE_BF16, false, s);
 }
 
-cudaError_t launch_unpack8_step(const spa2_pack8_tensor (&t)[2], const ColumnOrder& order, cudaStream_t s) {
-  Pack8Args a{};
-  std::copy(t, t + 2, a.t);
-  a.n = 2;
-  a.order = order;
-  const long long places = t[0].rows * t[0].d / CHUNK;  // whole groups: d is 64 or 128
+// What the backward on checkpoints starts from, by the row of the grid: 0 the largest |dO| of every
+// head, in DO_PARTS parts, 1 the order in which the dK/dV pass takes its columns, 2, 3 the kept
+// values of K and V as fp16 (exact where a group's largest is between 4e-6 and 65504; beyond,
+// clamped, and reported by the dK/dV pass if a query keeps them). The few blocks of the first two
+// rows work longest and start first.
+__global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_constant__ Unpack8Step a) {
+  if (blockIdx.y == 1) {
+    for (int head = blockIdx.x; head < a.heads; head += gridDim.x) longest_first(a.col_cnt, a.Tn, head, a.col_order);
+    return;
+  }
+  if (blockIdx.y == 0) {
+    __shared__ uint32_t most[THREADS / 32];
+    const long long chunks = a.per_head / CHUNK;
+    for (int item = blockIdx.x; item < a.heads * DO_PARTS; item += gridDim.x) {
+      const int head = item / DO_PARTS, part = item % DO_PARTS;
+      const uint4* x = static_cast<const uint4*>(a.dout) + head * chunks;
+      uint32_t m = 0;
+#pragma unroll 8
+      for (long long c = part * chunks / DO_PARTS + threadIdx.x; c < (part + 1) * chunks / DO_PARTS; c += THREADS) {
+        const uint4 w = x[c];
+        m = __vmaxu2(__vmaxu2(m, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
+        m = __vmaxu2(__vmaxu2(m, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
+      }
+      m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      if (lane_id() == 0) most[threadIdx.x / 32] = m;
+      __syncthreads();
+      if (threadIdx.x < 32) {
+        m = __reduce_max_sync(0xffffffffu, threadIdx.x < THREADS / 32 ? most[threadIdx.x] : 0u);
+        if (threadIdx.x == 0) a.do_most[item] = m << 16;
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  const bool second = blockIdx.y == 3;
+  const int8_t* codes = second ? a.v.codes : a.k.codes;
+  const uint8_t* exps = second ? a.v.exps : a.k.exps;
+  uint32_t* out = second ? a.v16 : a.k16;
+  const long long end = a.heads * a.per_head / CHUNK, base = (long long)blockIdx.x * PLACES + threadIdx.x;
+  uint2 code[UNROLL];
+  uint8_t E[UNROLL];
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const long long c = base + u * THREADS;
+    if (c < end) {
+      code[u] = reinterpret_cast<const uint2*>(codes)[c];
+      E[u] = exps[c / PER_GROUP];
+    }
+  }
+  bool clamped = false;
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const long long c = base + u * THREADS;
+    if (c >= end) continue;
+    const float step = pack8_step(E[u]);
+    float lo[4], hi[4], f[CHUNK];
+    pack8_floats(code[u].x, lo);
+    pack8_floats(code[u].y, hi);
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i) f[i] = (i < 4 ? lo[i & 3] : hi[i & 3]) * step;
+    store_f16(out + c * (CHUNK / 2), f, E[u], clamped);
+  }
+}
+
+cudaError_t launch_unpack8_step(const Unpack8Step& a, cudaStream_t s) {
+  const long long chunks = a.heads * a.per_head / CHUNK;
   KernelTimer kt(KID_UNPACK8, s);
-  unpack8_kernel<__nv_bfloat16, true, true><<<dim3((unsigned)((places + PLACES - 1) / PLACES), 3), THREADS, 0, s>>>(a);
+  unpack8_step_kernel<<<dim3((unsigned)((chunks + PLACES - 1) / PLACES), 4), THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
