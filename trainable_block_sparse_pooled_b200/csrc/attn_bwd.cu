@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_c
   const uint32_t tmem = sm.tmem_base;
   const WaitCtx wc{&sm.abort_flag, status, wait_limit_ns};
   const WaitCtx drain_wc{&sm.never, nullptr, wait_limit_ns};
+  if (KV16) pdl_wait();  // the rest reads what the dQ pass wrote
 
   if (warp == 8) {
     // ---------------- TMA producer: per column K_j, V_j, then its Q / dO tiles ----------------
@@ -979,10 +980,10 @@ static cudaError_t launch_dkdv(const BwdArgs& a, cudaStream_t s) {
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const int total_cols = a.BH * a.Tn;
   KernelTimer kt(KID_BWD_DKDV, s);
-  bwd_dkdv_kernel<D, TILED, KV16><<<dim3(std::min(total_cols, sms)), BWD_THREADS, smem, s>>>(
-      *a.tm_q16, *a.tm_k, *a.tm_v, *a.tm_do, a.lse, a.dvec, a.col_cnt, a.col_idx, a.col_order, a.unscale, a.ke, a.ve, a.dk, a.dv,
-      a.grad_f32, a.N, a.Tm, a.Tn, total_cols, a.ticket, a.scale, a.scale_log2, a.status, a.wait_limit_ns);
-  return cudaGetLastError();
+  return launch_k(bwd_dkdv_kernel<D, TILED, KV16>, dim3(std::min(total_cols, sms)), dim3(BWD_THREADS), smem, s,
+                  /*pdl=*/KV16, *a.tm_q16, *a.tm_k, *a.tm_v, *a.tm_do, a.lse, a.dvec, a.col_cnt, a.col_idx, a.col_order,
+                  a.unscale, a.ke, a.ve, a.dk, a.dv, a.grad_f32, a.N, a.Tm, a.Tn, total_cols, a.ticket, a.scale,
+                  a.scale_log2, a.status, a.wait_limit_ns);
 }
 
 // 3. dQ (q-major)

@@ -25,7 +25,17 @@
 // goes over S), so a second CTA on the SM works through its own chain meanwhile, and through
 // this one's start and end. That fixes the layout: 256 columns of tensor memory and 113 KB
 // of shared memory each, hence Q and dO in shared memory (SS products, bound by the 128
-// bytes a cycle that the tensor core reads there), K double-buffered and V single.
+// bytes a cycle that the tensor core reads there), K double-buffered and V single. At
+// [12, 32760, 128] with 25.6 of 512 blocks kept: 848 us; the products' shared-memory and tensor
+// cycles alone (768 a tile in the first pass, 1024 in the second, 531 tiles an SM) would take 560 us
+// at the 1.7 GHz that the power limit leaves. Measured and not kept: one CTA an SM with Q and dO in
+// tensor memory (as bwd_dq_kernel) 1000 us, that with 16 warps 1064; here, Q and dO in tensor memory
+// for the first pass 945 against 906, three buffers filled in turn by K and V 914 against 906.
+// The forward again for LSE and O (both halves of O stored and read, an fp16 V) took 333 + 34 + 50
+// us where the first pass, in bwd_dq_kernel's form, took 390.
+//
+// It starts while the decoding kernel ends (programmatic dependent launch): the setup, Q_i's codes and
+// the lists need nothing of it. The dK/dV pass starts in the same way behind this one.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -67,7 +77,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     bwd_dq_ckpt_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
                        const int8_t* __restrict__ q8, const uint8_t* __restrict__ qe, uint4* __restrict__ q16,
-                       uint4* __restrict__ do16, const uint32_t* __restrict__ do_most, float* __restrict__ unscale,
+                       uint4* __restrict__ do16, const uint32_t* do_most, float* __restrict__ unscale,
                        float* __restrict__ lse, float* __restrict__ dvec, const int* __restrict__ row_cnt, const int* __restrict__ row_idx,
                        int grad_f32, int N, int Tm, int Tn, float scale, float scale_log2, int* status,
                        unsigned long long wait_limit_ns) {
@@ -89,13 +99,13 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   const uint32_t lane = lane_id();
   const int i = blockIdx.x;
   const int bh = blockIdx.y;
+  pdl_trigger();
   const long long rowid = (long long)bh * Tm + i;
 
   // what the start waits for, asked for at once: the row's count and first block, and (warps
   // 0-7) Q_i's codes, 16 elements of a row at a time, neighbours in neighbouring threads
   constexpr int PER_ROW = D / 16, PIECES = 128 * PER_ROW / 256;
   const int count = row_cnt[rowid], first = row_idx[rowid * Tn];
-  const uint32_t most_part = do_most[(long long)bh * DO_PARTS + lane];
   uint4 code[PIECES];
   uint8_t E[PIECES];
   if (warp < 8) {
@@ -154,6 +164,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       tma_prefetch_desc(&tm_v);
       tma_prefetch_desc(&tm_do);
       const int end = 2 * n;
+      pdl_wait();  // K and V are decoded by the kernel before
       int kt = 0, vt = 0;  // tiles whose K, whose V has been started
       uint64_t t0 = 0;
       uint32_t idle = 0;
@@ -275,12 +286,6 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const long long row = (long long)i * 128 + r;
     const bool rvalid = row < N;
-    // the power of two that brings the head's largest |dO|, 2^(E - 127) or more, into [4, 8): its
-    // exponent field is 127 + 129 - E (for infinities and NaN, which are reported, and zeros any will do)
-    const uint32_t most_e = min(max(__reduce_max_sync(0xffffffffu, most_part) >> 23, 29u), 227u);
-    const float do_scale = __uint_as_float((256u - most_e) << 23);
-    const float back = __uint_as_float((most_e - 2u) << 23);  // its inverse
-    if (i == 0 && threadIdx.x == 0) unscale[bh] = back;
     // Q_i from its codes into shared memory, and its fp16 copy
     bool bad = false;
 #pragma unroll
@@ -309,6 +314,16 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     }
     fence_proxy_async_smem();
     mbar_arrive(&sm.q_ready);
+    // do_most is written by the kernel before: waited for, and loaded as volatile (the compiler may move
+    // a plain load of read-only memory above the wait)
+    pdl_wait();
+    const uint32_t most = reinterpret_cast<const volatile uint32_t*>(do_most)[(long long)bh * DO_PARTS + lane];
+    // the power of two that brings the head's largest |dO|, 2^(E - 127) or more, into [4, 8): its
+    // exponent field is 127 + 129 - E (for infinities and NaN, which are reported, and zeros any will do)
+    const uint32_t most_e = min(max(__reduce_max_sync(0xffffffffu, most) >> 23, 29u), 227u);
+    const float do_scale = __uint_as_float((256u - most_e) << 23);
+    const float back = __uint_as_float((most_e - 2u) << 23);  // its inverse
+    if (i == 0 && threadIdx.x == 0) unscale[bh] = back;
     // dO_i to fp16 in place, 8 elements of a row at a time, and its copy
     if (n > 0 && wait_warp(&sm.do_full, 0, wc)) {
 #pragma unroll
@@ -516,10 +531,10 @@ static cudaError_t launch_dq_ckpt_t(const BwdArgs& a, cudaStream_t s) {
                                              (int)smem);
   if (e != cudaSuccess) return e;
   KernelTimer kt(KID_BWD_DQ_CKPT, s);
-  bwd_dq_ckpt_kernel<D, TILED><<<dim3(a.Tm, a.BH), DQC_THREADS, smem, s>>>(
-      *a.tm_dob, *a.tm_k, *a.tm_v, *a.tm_dq, a.q8, a.qe, static_cast<uint4*>(a.q16), static_cast<uint4*>(a.do16), a.do_most, a.unscale, a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N,
-      a.Tm, a.Tn, a.scale, a.scale_log2, a.status, a.wait_limit_ns);
-  return cudaGetLastError();
+  return launch_k(bwd_dq_ckpt_kernel<D, TILED>, dim3(a.Tm, a.BH), dim3(DQC_THREADS), smem, s, true, *a.tm_dob, *a.tm_k,
+                  *a.tm_v, *a.tm_dq, a.q8, a.qe, static_cast<uint4*>(a.q16), static_cast<uint4*>(a.do16), a.do_most,
+                  a.unscale, a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N, a.Tm, a.Tn, a.scale, a.scale_log2,
+                  a.status, a.wait_limit_ns);
 }
 
 cudaError_t launch_dq_ckpt(const BwdArgs& a, int d, cudaStream_t s) {

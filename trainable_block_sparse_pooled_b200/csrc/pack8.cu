@@ -3,13 +3,22 @@
 // biased fp32 exponent of their largest magnitude; code = rint(x * 2^(133 - E)),
 // value = code * 2^(E - 133).
 //
-// Both kernels move bytes and little else (bf16: 3 + 1/32 bytes per element). Eight
-// elements of a row are a chunk (one 16-byte access, two for fp32), four chunks a group;
-// a thread takes UNROLL chunks, 256 apart, and loads them all before it works on the
+// Both kernels move bytes and little else (bf16: 3 + 1/32 bytes per element): bound by HBM. Eight
+// elements of a row are a chunk (one 16-byte access, two for fp32), four chunks a
+// group; a thread takes UNROLL chunks, 256 apart, and loads them all before it works on the
 // first, so that enough of them are in flight to cover HBM's latency. The group's largest
-// exponent meets over two shuffles.
+// exponent meets over two shuffles. Measured, four tensors [393120, 128] bf16 (610 MB each way):
+// pack 94 us, unpack 88 us = 6.5 and 6.9 TB/s with the 126 MB that L2 still holds of the last
+// pass, 0.94 of the measured copy rate over both; UNROLL 4 against 1, 2, 8: 100 + 92 us (from cold
+// L2) against 124 + 113, 111 + 95, 125 + 108. A ragged fp16 tensor [32760, 1000] 23 + 17 us, for
+// 15 us of bytes each: two microseconds of start, and blocks in 7 waves.
+// Where tensors fit in L2 the instructions count as well: a code costs a conversion, a fused
+// multiply-add and half a clamp of a 16-bit pair, its value a byte permutation, an addition and a
+// product (no integer conversions, which run at a quarter of the rate).
 // pack8_kernel, unpack8_kernel                rows that 16-byte accesses fit
-// pack8_single_kernel, unpack8_single_kernel  any others: one lane per element
+// pack8_single_kernel, unpack8_single_kernel  any others: one lane per element (ten times slower:
+//                                             1033 + 1006 us on the tensors above)
+// unpack8_step_kernel                         what the attention's backward starts from
 #include <algorithm>
 
 #include "common.cuh"
@@ -102,6 +111,9 @@ SPA2_DEV void store_f16(uint32_t* to, const float (&f)[CHUNK], uint32_t E, bool&
 
 }  // namespace
 
+// FLAT, rows of whole groups, needs no division: 100 + 92 us against 117 + 102 on the tensors above.
+// There six blocks to an SM (40 registers) gain 3%; with ragged rows they would cost 20%, and fp32
+// chunks would spill.
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) pack8_kernel(const __grid_constant__ Pack8Args a) {
   pdl_trigger();
@@ -253,8 +265,10 @@ cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* s
 // head, in DO_PARTS parts, 1 the order in which the dK/dV pass takes its columns, 2, 3 the kept
 // values of K and V as fp16 (exact where a group's largest is between 4e-6 and 65504; beyond,
 // clamped, and reported by the dK/dV pass if a query keeps them). The few blocks of the first two
-// rows work longest and start first.
+// rows work longest and start first (last, they would end 15 us after the others). 60 us at
+// [12, 32760, 128], for 404 MB: the measured copy rate.
 __global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_constant__ Unpack8Step a) {
+  pdl_trigger();
   if (blockIdx.y == 1) {
     for (int head = blockIdx.x; head < a.heads; head += gridDim.x) longest_first(a.col_cnt, a.Tn, head, a.col_order);
     return;
