@@ -519,13 +519,17 @@ SPA2_DEV float fast_exp2(float x) {
 // dK/dV pass takes its columns head by head and, within a head, long columns
 // first: it does not end on a long column, and the Q / dO tiles the running
 // columns share stay within one head's worth of L2.
-SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* __restrict__ order) {
+// early > 0: the `early` longest columns of every head come before all others (rank by
+// rank), so that a column that most query blocks keep (attention sinks) does not start when the
+// rest is nearly done.
+SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* __restrict__ order, int heads = 0,
+                            int early = 0) {
   constexpr int KEYS = 1024, PER = KEYS / 256;
   __shared__ int start[KEYS];
   __shared__ int warp_sum[8];
   const int t = threadIdx.x;
   const int* cnt_h = cnt + (long long)head * Tn;
-  int* out_h = order + (long long)head * Tn;
+  int* out_h = order + (long long)early * heads + (long long)head * (Tn - early) - early;
   for (int k = t; k < KEYS; k += 256) start[k] = 0;
   __syncthreads();
   for (int c = t; c < Tn; c += 256) atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
@@ -553,8 +557,10 @@ SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* 
     base += bin[e];
   }
   __syncthreads();
-  for (int c = t; c < Tn; c += 256)
-    out_h[atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1)] = head * Tn + c;
+  for (int c = t; c < Tn; c += 256) {
+    const int rank = atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
+    (rank < early ? order[(long long)rank * heads + head] : out_h[rank]) = head * Tn + c;
+  }
   __syncthreads();  // start[] is reused by the next head of this block
 }
 

@@ -38,6 +38,7 @@ struct Pack8Args {
 
 constexpr int CHUNK = 8, PER_GROUP = 4, UNROLL = 4, THREADS = 256;
 constexpr int PLACES = UNROLL * THREADS;  // chunk places of a block
+constexpr int EARLY_COLUMNS = 8;          // a head's columns that the dK/dV pass takes before all others
 
 template <typename T>
 struct alignas(16) Chunk {
@@ -270,7 +271,7 @@ cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* s
 __global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_constant__ Unpack8Step a) {
   pdl_trigger();
   if (blockIdx.y == 1) {
-    for (int head = blockIdx.x; head < a.heads; head += gridDim.x) longest_first(a.col_cnt, a.Tn, head, a.col_order);
+    for (int head = blockIdx.x; head < a.heads; head += gridDim.x) longest_first(a.col_cnt, a.Tn, head, a.col_order, (int)a.heads, min(a.Tn, EARLY_COLUMNS));
     return;
   }
   if (blockIdx.y == 0) {
