@@ -414,6 +414,27 @@ def test_every_count_of_kept_blocks(N, d, bq, bkv):
     against_oracle(q, k, v, dout, lists(keep), bq, bkv)
 
 
+@pytest.mark.parametrize("N,d,bq,bkv", [(4500, 64, 128, 64), (6000, 128, 128, 64), (4500, 128, 64, 64)])
+def test_columns_that_every_query_block_keeps(N, d, bq, bkv):
+    """Few heads and long columns: gathered from parts. The first block is kept by all query blocks, others by
+    half, a quarter, an eighth of them and by one; the ragged last one by 33."""
+    q, k, v = synth.gaussian_with_sinks(B=1, H=1, N=N, d=d, seed=N + d, device="cuda")
+    dout = synth.normal_like(q.shape, seed=N, device="cuda")
+    Tm, Tn = b.block_counts(N, bq, bkv)
+    keep = torch.zeros(1, 1, Tm, Tn, dtype=torch.bool)
+    for column, step in ((0, 1), (1, 2), (2, 4), (3, 8)):
+        keep[..., ::step, column] = True
+    keep[0, 0, torch.arange(Tm), torch.arange(Tm) * bq // bkv] = True
+    keep[..., :33, Tn - 1] = True
+    m = lists(keep)
+    got = against_oracle(q, k, v, dout, m, bq, bkv)
+    assert all(torch.equal(a, c) for a, c in zip(got, attention(q, k, v, dout, m, bq, bkv)))
+    s = b.Spa2(1, 1, N, d, bq=bq, bkv=bkv)
+    grads = s.bwd_ckpt(pack8(q, k, v), dout, m)      # fp32
+    s.check()
+    assert all(torch.equal(a, c.to(BF16)) for a, c in zip(got[1:], grads))
+
+
 def test_more_than_2_31_elements_in_the_attention():
     """The last heads of a problem of more than 2^31 elements, against the same heads alone, bit for bit."""
     H, N, d = 130, 131072, 128

@@ -2,6 +2,7 @@
 // workspace layout, TMA descriptor construction and kernel launches. No entry
 // point allocates device memory; every buffer, the workspace included, belongs
 // to the caller.
+#include <algorithm>
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -155,6 +156,8 @@ struct CkptWs {
   void *k16, *v16;    // [BH, N, d] fp16
   uint32_t* do_most;  // [BH, DO_PARTS]
   float* unscale;     // [BH]
+  ColumnSplit split;
+  int* col_order;     // with the entries of split columns
   size_t bytes;
 };
 static CkptWs ckpt_ws(void* ws, const Shape& s) {
@@ -172,6 +175,18 @@ static CkptWs ckpt_ws(void* ws, const Shape& s) {
   off += al256((size_t)s.BH * DO_PARTS * 4);
   w.unscale = reinterpret_cast<float*>(base + off);
   off += al256((size_t)s.BH * 4);
+  // A column that every query block keeps is a chain of TMt tiles, and a pass takes about BH * kept /
+  // 148 columns' worth: with few heads the chain would outlast the rest, with many it does not matter
+  const bool split = s.BH <= 32 && s.TMt >= 32;
+  w.split.ranks = split ? std::min(s.TNt, 4) : 0;
+  w.split.parts = split ? 4 : 1;
+  w.split.heads = (int)s.BH;
+  w.split.partial = reinterpret_cast<float*>(base + off);
+  off += al256((size_t)s.BH * w.split.ranks * w.split.parts * 2 * 64 * s.d * 4);
+  w.split.done = reinterpret_cast<int*>(base + off);
+  off += al256((size_t)s.BH * w.split.ranks * 4 * 4);
+  w.col_order = reinterpret_cast<int*>(base + off);
+  off += al256((size_t)s.BH * (s.TNt + w.split.ranks * (w.split.parts - 1)) * 4);
   w.bytes = off;
   return w;
 }
@@ -548,12 +563,12 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
     ci = t.csc_idx;
   }
   SPA2_CUDA_TRY(launch_unpack8_step(Unpack8Step{*k8, *v8, static_cast<uint32_t*>(w.k16), static_cast<uint32_t*>(w.v16),
-                                                dout, w.do_most, cc, w.b.col_order, s.TNt, s.BH, (long long)s.N * d},
+                                                dout, w.do_most, cc, w.col_order, s.TNt, w.split, s.BH, (long long)s.N * d},
                                     st));
   BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, nullptr, nullptr, nullptr, dout, nullptr, w.lse, rc, ri, cc, ci,
             w.b.dvec, w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
-            scale * 1.4426950408889634f, status, status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.b.col_order,
-            q8->codes, q8->exps, k8->exps, v8->exps, &tdob, w.do_most, w.unscale};
+            scale * 1.4426950408889634f, status, status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.col_order,
+            q8->codes, q8->exps, k8->exps, v8->exps, &tdob, w.do_most, w.unscale, w.split};
   SPA2_CUDA_TRY(launch_bwd(a, d, st));
   return SPA2_OK;
 }

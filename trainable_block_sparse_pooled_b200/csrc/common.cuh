@@ -521,15 +521,17 @@ SPA2_DEV float fast_exp2(float x) {
 // columns share stay within one head's worth of L2.
 // early > 0: the `early` longest columns of every head come before all others (rank by
 // rank), so that a column that most query blocks keep (attention sinks) does not start when the
-// rest is nearly done.
+// rest is nearly done. Of these the first `ranks` are listed `parts` times, for the parts of
+// their tiles: order has heads * (Tn + ranks * (parts - 1)) entries.
 SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* __restrict__ order, int heads = 0,
-                            int early = 0) {
+                            int early = 0, int ranks = 0, int parts = 1) {
   constexpr int KEYS = 1024, PER = KEYS / 256;
   __shared__ int start[KEYS];
   __shared__ int warp_sum[8];
   const int t = threadIdx.x;
   const int* cnt_h = cnt + (long long)head * Tn;
-  int* out_h = order + (long long)early * heads + (long long)head * (Tn - early) - early;
+  const int more = ranks * (parts - 1);  // entries of a head beyond one per column
+  int* out_h = order + (long long)(early + more) * heads + (long long)head * (Tn - early) - early;
   for (int k = t; k < KEYS; k += 256) start[k] = 0;
   __syncthreads();
   for (int c = t; c < Tn; c += 256) atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
@@ -559,7 +561,11 @@ SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* 
   __syncthreads();
   for (int c = t; c < Tn; c += 256) {
     const int rank = atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
-    (rank < early ? order[(long long)rank * heads + head] : out_h[rank]) = head * Tn + c;
+    if (rank < ranks) {
+      for (int x = 0; x < parts; ++x) order[(long long)(rank * parts + x) * heads + head] = head * Tn + c;
+    } else {
+      (rank < early ? order[(long long)(rank + more) * heads + head] : out_h[rank]) = head * Tn + c;
+    }
   }
   __syncthreads();  // start[] is reused by the next head of this block
 }

@@ -86,6 +86,13 @@ cudaError_t launch_fwd(const FwdArgs& a, int d, cudaStream_t s);
 cudaError_t launch_v_to_f16(const void* v, void* v16, long long elems, int* status, cudaStream_t s);
 
 // attn_bwd.cu
+// The backward on 8-bit checkpoints: the `ranks` longest columns of every head are taken by the dK/dV
+// pass in up to `parts` parts, whose sums meet in `partial` [ranks * heads, parts, 2, 16, d, 4]
+struct ColumnSplit {
+  int ranks, parts, heads;
+  float* partial;
+  int* done;  // [ranks * heads, 4]: parts that are there, by quarter of 32 features; zero before the pass
+};
 struct BwdArgs {
   const CUtensorMap* tm_q;    // Q bf16, box {64, 128, 1}
   const CUtensorMap* tm_k;    // K bf16, box {64, 64, 1}
@@ -126,6 +133,7 @@ struct BwdArgs {
   const CUtensorMap* tm_dob;  // dO bf16, box {64, 128, 1}
   const uint32_t* do_most;    // [BH, DO_PARTS]
   float* unscale;             // [BH]: do16 and dvec are dO and D divided by this power of two
+  ColumnSplit split;
 };
 cudaError_t launch_bwd(const BwdArgs& a, int d, cudaStream_t s);
 
@@ -145,6 +153,7 @@ struct Unpack8Step {
   const int* col_cnt;
   int* col_order;
   int Tn;
+  ColumnSplit split;
   long long heads, per_head;  // N * d elements to a head
 };
 cudaError_t launch_unpack8_step(const Unpack8Step& a, cudaStream_t s);

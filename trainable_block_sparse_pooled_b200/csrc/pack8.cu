@@ -271,7 +271,11 @@ cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* s
 __global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_constant__ Unpack8Step a) {
   pdl_trigger();
   if (blockIdx.y == 1) {
-    for (int head = blockIdx.x; head < a.heads; head += gridDim.x) longest_first(a.col_cnt, a.Tn, head, a.col_order, (int)a.heads, min(a.Tn, EARLY_COLUMNS));
+    for (int head = blockIdx.x; head < a.heads; head += gridDim.x) {
+      longest_first(a.col_cnt, a.Tn, head, a.col_order, (int)a.heads, min(a.Tn, EARLY_COLUMNS), a.split.ranks,
+                    a.split.parts);
+      if (threadIdx.x < a.split.ranks * 4) a.split.done[(threadIdx.x / 4 * a.heads + head) * 4 + threadIdx.x % 4] = 0;
+    }
     return;
   }
   if (blockIdx.y == 0) {
