@@ -435,6 +435,17 @@ def test_columns_that_every_query_block_keeps(N, d, bq, bkv):
     assert all(torch.equal(a, c.to(BF16)) for a, c in zip(got[1:], grads))
 
 
+def test_the_same_bits_when_all_columns_are_alike():
+    """Every column is as long as every other: which of them are taken in parts must not depend on chance."""
+    q, k, v = synth.gaussian_with_sinks(B=1, H=3, N=4352, d=64, seed=23, device="cuda")
+    dout = synth.normal_like(q.shape, seed=24, device="cuda")
+    m = lists(torch.ones(1, 3, 34, 68, dtype=torch.bool))
+    want = attention(q, k, v, dout, m)
+    for _ in range(6):
+        assert all(torch.equal(a, c) for a, c in zip(attention(q, k, v, dout, m), want))
+    check_errors()
+
+
 def test_more_than_2_31_elements_in_the_attention():
     """The last heads of a problem of more than 2^31 elements, against the same heads alone, bit for bit."""
     H, N, d = 130, 131072, 128

@@ -178,7 +178,7 @@ static CkptWs ckpt_ws(void* ws, const Shape& s) {
   // A column that every query block keeps is a chain of TMt tiles, and a pass takes about BH * kept /
   // 148 columns' worth: with few heads the chain would outlast the rest, with many it does not matter
   const bool split = s.BH <= 32 && s.TMt >= 32;
-  w.split.ranks = split ? std::min(s.TNt, 4) : 0;
+  w.split.ranks = split ? std::min(s.TNt, MAX_RANKS) : 0;
   w.split.parts = split ? 4 : 1;
   w.split.heads = (int)s.BH;
   w.split.partial = reinterpret_cast<float*>(base + off);

@@ -521,20 +521,48 @@ SPA2_DEV float fast_exp2(float x) {
 // columns share stay within one head's worth of L2.
 // early > 0: the `early` longest columns of every head come before all others (rank by
 // rank), so that a column that most query blocks keep (attention sinks) does not start when the
-// rest is nearly done. Of these the first `ranks` are listed `parts` times, for the parts of
-// their tiles: order has heads * (Tn + ranks * (parts - 1)) entries.
+// rest is nearly done. Of these the first `ranks` (of equal columns the lower ones: whether a column
+// is taken in parts decides how its sums are rounded, so it must not depend on the atomics) are
+// listed `parts` times, for the parts of their tiles: order has heads * (Tn + ranks * (parts - 1))
+// entries.
+constexpr int MAX_RANKS = 4;
 SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* __restrict__ order, int heads = 0,
                             int early = 0, int ranks = 0, int parts = 1) {
   constexpr int KEYS = 1024, PER = KEYS / 256;
   __shared__ int start[KEYS];
   __shared__ int warp_sum[8];
+  __shared__ unsigned long long warp_most[8];
+  __shared__ int chosen[MAX_RANKS];
   const int t = threadIdx.x;
   const int* cnt_h = cnt + (long long)head * Tn;
   const int more = ranks * (parts - 1);  // entries of a head beyond one per column
   int* out_h = order + (long long)(early + more) * heads + (long long)head * (Tn - early) - early;
+  auto is_chosen = [&](int c, int n) {
+    bool is = false;
+    for (int x = 0; x < n; ++x) is = is || chosen[x] == c;
+    return is;
+  };
+  for (int rank = 0; rank < ranks; ++rank) {  // ranks <= Tn: there is one left
+    unsigned long long most = 0;
+    for (int c = t; c < Tn; c += 256)
+      if (!is_chosen(c, rank))
+        most = max(most, (unsigned long long)(min(max(cnt_h[c], 0), KEYS - 1) + 1) << 32 | (0xffffffffu - (uint32_t)c));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if ((t & 31) == 0) warp_most[t >> 5] = most;
+    __syncthreads();
+    if (t == 0) {
+      for (int w = 1; w < 8; ++w) most = max(most, warp_most[w]);
+      const int c = (int)(0xffffffffu - (uint32_t)most);
+      chosen[rank] = c;
+      for (int x = 0; x < parts; ++x) order[(long long)(rank * parts + x) * heads + head] = head * Tn + c;
+    }
+    __syncthreads();
+  }
   for (int k = t; k < KEYS; k += 256) start[k] = 0;
   __syncthreads();
-  for (int c = t; c < Tn; c += 256) atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
+  for (int c = t; c < Tn; c += 256)
+    if (!is_chosen(c, ranks)) atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
   __syncthreads();
   // exclusive scan in descending key order: thread t owns keys KEYS-1-PER*t ... KEYS-PER-PER*t
   int bin[PER], sum = 0;
@@ -560,12 +588,9 @@ SPA2_DEV void longest_first(const int* __restrict__ cnt, int Tn, int head, int* 
   }
   __syncthreads();
   for (int c = t; c < Tn; c += 256) {
-    const int rank = atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
-    if (rank < ranks) {
-      for (int x = 0; x < parts; ++x) order[(long long)(rank * parts + x) * heads + head] = head * Tn + c;
-    } else {
-      (rank < early ? order[(long long)(rank + more) * heads + head] : out_h[rank]) = head * Tn + c;
-    }
+    if (is_chosen(c, ranks)) continue;
+    const int rank = ranks + atomicAdd(&start[min(max(cnt_h[c], 0), KEYS - 1)], 1);
+    (rank < early ? order[(long long)(rank + more) * heads + head] : out_h[rank]) = head * Tn + c;
   }
   __syncthreads();  // start[] is reused by the next head of this block
 }

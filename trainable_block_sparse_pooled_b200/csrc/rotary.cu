@@ -8,8 +8,8 @@
 // an fp64 product and reduction and an fp32 sincospi, some 60 instructions a pair; one thread
 // takes its unit through every head, so that they are paid once per token, not per head, and
 // steps its pointers from head to head (recomputing 64-bit addresses made the kernel
-// issue-bound: 15 instructions per element, 92 us against 68 below). Four heads' loads are in
-// flight at a time. One launch turns q and k: 24 heads share a token's angles at 12 + 12 heads.
+// issue-bound: 15 instructions per element, 92 us against 68 below). One launch turns q and k,
+// whose heads share their tokens' angles.
 // Measured (q and k, one launch): [1, 40, 75600, 128] bf16 each 490 us = 6.3 TB/s, 0.96 of the
 // measured copy rate; [1, 12, 32760, 128] each 68 us = 6.0 TB/s (4.6 waves of blocks).
 #include <algorithm>
@@ -42,6 +42,7 @@ struct RotaryArgs {
   // units of a row are `turned` such and then copied ones
   int units, turned, step, partner;
   int per_block;  // heads of a block
+  uint32_t units_mul, units_shift, n_mul, n_shift;  // x / units, x / N for x < 2^31 (shift 32: see divisor)
 };
 
 template <typename T>
@@ -85,28 +86,55 @@ SPA2_DEV void turn(float x, float y, float2 cs, float& ox, float& oy) {
 }  // namespace
 
 // SPLIT: a unit is V elements and their V partners elsewhere in the row (the half layout; single
-// elements of the interleaved one). One block asked for per SM leaves the compiler 78 registers and
-// the loads of four heads together (three blocks fit): 490 us at the 14B shape above; unasked it
-// took 66 registers and 580 us, four blocks' worth (64) 524, two heads at a time 501 to 519, eight
-// 493 to 684.
+// elements of the interleaved one).
+// Registers against loads in flight, measured: the interleaved units do best with four heads' loads
+// together and 78 registers (three blocks an SM): 490 us at the 14B shape above; with no block count
+// asked for the compiler took 66 registers and 580 us, with four blocks (64) 524, two heads at a time
+// 501 to 519, eight 493 to 684. SPLIT units hold twice the angles: one head (two loads) at a time and
+// four blocks an SM (64 registers) take 80 us for [1, 12, 32760, 128] twice, two heads and two blocks
+// (88 registers) 109, five blocks (48, spilling) 88; units of 8 bytes do best with five.
+// Loading a batch ahead of the one at work gained 3 us there and lost 20 in the interleaved form.
 template <typename T, int V, bool SPLIT>
-__global__ void __launch_bounds__(256, 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(256, SPLIT ? (V == 8 ? 4 : 5) : 1) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int PAIRS = SPLIT ? V : V / 2;  // pairs of a unit
-  constexpr int HB = SPLIT ? 2 : 4;         // heads in flight: 4 loads
+  constexpr int HB = SPLIT ? 1 : 4;         // heads in flight
   using VT = Vec<T, V>;
   const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long token = idx / a.units;
-  if (token >= a.tokens) return;
-  const int u = (int)(idx - token * a.units);
-  const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
-  const bool copy = u >= a.turned;
+  const int token = a.units_shift < 32 ? (int)(__umulhi((uint32_t)idx, a.units_mul) >> a.units_shift)
+                                       : (int)min(idx / a.units, a.tokens);
+  const bool there = token < a.tokens;
+  const int u = (int)(idx - (long long)token * a.units);
+  const int b = a.n_shift < 32 ? (int)(__umulhi((uint32_t)token, a.n_mul) >> a.n_shift) : token, n = token - b * a.N;
+  const bool copy = u >= a.turned || !there;
   const int e0 = copy ? a.rd + (u - a.turned) * V : u * a.step;
   const int e1 = e0 + a.partner;
   float2 cs[PAIRS];
-  if (!copy) {
+  if (a.turned == a.units) {
+    if (there) {
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) cs[i] = cos_sin(a, b, n, u * PAIRS + i);
+      for (int i = 0; i < PAIRS; ++i) cs[i] = cos_sin(a, b, n, u * PAIRS + i);
+    }
+  } else {
+    // part of the head: the warp shares the angles of its few turning threads out evenly (an
+    // eighth of 64 elements turned, 4 heads: 67 us a launch, 82 with every thread on its own)
+    __shared__ float2 angle[8][32 * PAIRS];
+    __shared__ int3 unit[8][32];
+    const int w = threadIdx.x >> 5;
+    const uint32_t turning = __ballot_sync(0xffffffffu, !copy);
+    const int place = __popc(turning & ((1u << lane_id()) - 1u));
+    if (!copy) unit[w][place] = make_int3(b, n, u * PAIRS);
+    __syncwarp();
+    for (int k = lane_id(); k < __popc(turning) * PAIRS; k += 32) {
+      const int3 at = unit[w][k / PAIRS];
+      angle[w][k] = cos_sin(a, at.x, at.y, at.z + k % PAIRS);
+    }
+    __syncwarp();
+    if (!copy) {
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) cs[i] = angle[w][place * PAIRS + i];
+    }
   }
+  if (!there) return;
   const int first = blockIdx.y * a.per_block, last = min(a.heads, first + a.per_block);
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {  // this block's heads of the first tensor, then of the second
@@ -149,6 +177,15 @@ __global__ void __launch_bounds__(256, 1) rotary_kernel(const __grid_constant__ 
   }
 }
 
+// x / d = (x * mul >> 32) >> shift for x < 2^31: mul = ceil(2^(31 + l) / d) with 2^l the power of two
+// from d on; for d = 1 it does not fit in 32 bits, and shift 32 says so
+static void divisor(long long d, uint32_t& mul, uint32_t& shift) {
+  uint32_t l = 0;
+  while ((1LL << l) < d) ++l;
+  mul = d == 1 ? 0u : (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+  shift = d == 1 ? 32u : l - 1;
+}
+
 template <typename T, int V, bool SPLIT>
 static cudaError_t launch_rotary(RotaryArgs a, bool half, cudaStream_t s) {
   a.step = SPLIT && !half ? 2 : V;
@@ -157,6 +194,9 @@ static cudaError_t launch_rotary(RotaryArgs a, bool half, cudaStream_t s) {
   a.units = a.turned + (a.d - a.rd) / V;
   const long long blocks = (a.tokens * a.units + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  divisor(a.units, a.units_mul, a.units_shift);
+  if (blocks * 256 > 0x7fffffffLL) a.units_shift = 32;
+  divisor(a.N, a.n_mul, a.n_shift);
   // One block takes all heads of its tokens, so that angles are computed once; with few tokens
   // the heads are split over blocks until there are about 8 for every SM. Unsplit and split, us:
   // 8 tokens of 40 heads 34.5 / 9.2, 1000 tokens of 24 heads 26.4 / 13.3, 4000 of 24 18.6 / 19.6
