@@ -334,8 +334,9 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
  * take fp16 operands and add up in fp32: the kept values (exact where a group's
  * largest magnitude is between 4e-6 and 65504; beyond, clamped and reported as
  * SPA2_ERR_RANGE), P and dS (11 bits each), and dO times a power of two per head
- * that brings the head's largest |dO| into [4, 8), so that gradients of any size
- * keep their precision (infinities and NaN are reported as SPA2_ERR_RANGE).
+ * that brings the head's largest |dO| into [4, 8), lower where |V| is above 16 (so
+ * that dS stays in range): gradients of any size keep their precision (infinities
+ * and NaN are reported as SPA2_ERR_RANGE).
  * Keeping O and LSE instead of recomputing them is cheaper but not close: with q,
  * k, v rounded to 8 bits and O, LSE not, the rows of dS no longer sum to zero,
  * and sink keys of 8x norm amplify that to 12% of dQ (4% with recomputation).

@@ -334,6 +334,24 @@ def test_gradients_scale_with_dout():
     assert not any(x.any() for x in zero)
 
 
+def test_large_values():
+    """v times 2^8 or 2^11 gives dq and dk times as much and the same dv, where dS would leave a half's range
+    if dO kept its own. dO is scaled down by up to 2^10 then: its small elements lose at most
+    2^-25 of a largest of 2^-7 or more, and dS as much, 4e-6 of the largest; the results may round to the
+    other neighbour, one bf16 step (twice half a step), and near zero differ by 1e-4 of the largest."""
+    q, k, v = synth.gaussian_with_sinks(B=1, H=2, N=512, d=128, seed=25, device="cuda")
+    dout = synth.normal_like(q.shape, seed=26, device="cuda")
+    m = block_mask(q, k, 0.4, 0.6)
+    want = attention(q, k, v, dout, m)[1:]
+    for power in (8, 11):
+        got = attention(q, k, torch.ldexp(v.float(), torch.tensor(power, device="cuda")).to(BF16), dout, m)[1:]
+        check_errors()
+        for a, w, times in zip(got, want, (2.0 ** -power, 2.0 ** -power, 1.0)):
+            a, w = f64(a) * times, f64(w)
+            assert np.isfinite(a).all()
+            assert (np.abs(a - w) <= 2 * bf16_half_ulp(w) + 1e-4 * np.abs(w).max()).all()
+
+
 def test_small_rows_beside_large_ones():
     """Rows of dout at 2^-12 of the others: what they alone contribute, the values' gradients of a key
     block that only they keep. With the head's largest |dout| in [4, 8) (here it is: no scaling)

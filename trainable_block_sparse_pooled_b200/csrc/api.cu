@@ -563,7 +563,7 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
     ci = t.csc_idx;
   }
   SPA2_CUDA_TRY(launch_unpack8_step(Unpack8Step{*k8, *v8, static_cast<uint32_t*>(w.k16), static_cast<uint32_t*>(w.v16),
-                                                dout, w.do_most, cc, w.col_order, s.TNt, w.split, s.BH, (long long)s.N * d},
+                                                dout, w.do_most, cc, w.col_order, s.N, d, s.TNt, w.split, s.BH, (long long)s.N * d},
                                     st));
   BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, nullptr, nullptr, nullptr, dout, nullptr, w.lse, rc, ri, cc, ci,
             w.b.dvec, w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,

@@ -15,8 +15,9 @@
 // Precision: every product takes fp16 operands and adds up in fp32, in this pass as in the dK/dV
 // pass. The kept values have 7 bits and are exact in fp16 (a group whose largest magnitude is
 // below 4e-6 loses up to 2^-25; above 65504 is clamped and reported). dO is multiplied by a power
-// of two per head that brings the head's largest |dO| into [4, 8) (gradients are linear in dO; the
-// loss's scale must not decide what is left of them), which leaves its 8 bits exact down to 2^-19 of
+// of two per head that brings the head's largest |dO| into [4, 8) (lower where V is above 16: dS must
+// not leave fp16's range; gradients are linear in dO, and the loss's scale must not decide what is
+// left of them), which leaves its 8 bits exact down to 2^-19 of
 // the largest. dS, formed in fp32, is rounded to 11 bits, as the dK/dV pass rounds it: relative to
 // dQ's norm 2e-4 in random rows and 8e-4 with sink keys of 8x norm, whose terms cancel, against
 // 1.65e-3 of bf16 gradients.
@@ -318,9 +319,13 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     // a plain load of read-only memory above the wait)
     pdl_wait();
     const uint32_t most = reinterpret_cast<const volatile uint32_t*>(do_most)[(long long)bh * DO_PARTS + lane];
-    // the power of two that brings the head's largest |dO|, 2^(E - 127) or more, into [4, 8): its
-    // exponent field is 127 + 129 - E (for infinities and NaN, which are reported, and zeros any will do)
-    const uint32_t most_e = min(max(__reduce_max_sync(0xffffffffu, most) >> 23, 29u), 227u);
+    // The power of two that brings the head's largest |dO|, 2^(E - 127) or more, into [4, 8): its
+    // exponent field is 127 + 129 - E (for infinities and NaN, which are reported, and zeros any will
+    // do). With |V| < 2^(F - 126), F its largest exponent, |dP - D| < d 2^(F - 122) then, and where that
+    // could pass 2^15 dO is scaled down further, so that dS stays within fp16's range.
+    const int v_e = (int)__reduce_max_sync(0xffffffffu, most & 0xffffu);
+    const uint32_t down = (uint32_t)max(0, v_e - 137 + (D == 128 ? 7 : 6));
+    const uint32_t most_e = min(max(__reduce_max_sync(0xffffffffu, most) >> 23, 29u) + down, 227u);
     const float do_scale = __uint_as_float((256u - most_e) << 23);
     const float back = __uint_as_float((most_e - 2u) << 23);  // its inverse
     if (i == 0 && threadIdx.x == 0) unscale[bh] = back;

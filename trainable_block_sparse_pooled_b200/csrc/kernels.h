@@ -149,10 +149,10 @@ struct Unpack8Step {
   spa2_pack8_tensor k, v;
   uint32_t *k16, *v16;
   const void* dout;   // bf16, 16-byte aligned
-  uint32_t* do_most;  // [heads, DO_PARTS] fp32 bits
+  uint32_t* do_most;  // [heads, DO_PARTS]: the largest |dO|'s bf16 bits, and in the low half V's largest exponent
   const int* col_cnt;
   int* col_order;
-  int Tn;
+  int N, d, Tn;
   ColumnSplit split;
   long long heads, per_head;  // N * d elements to a head
 };

@@ -263,7 +263,7 @@ cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* s
 }
 
 // What the backward on checkpoints starts from, by the row of the grid: 0 the largest |dO| of every
-// head, in DO_PARTS parts, 1 the order in which the dK/dV pass takes its columns, 2, 3 the kept
+// head and the largest exponent of V in the blocks that a query keeps, in DO_PARTS parts, 1 the order in which the dK/dV pass takes its columns, 2, 3 the kept
 // values of K and V as fp16 (exact where a group's largest is between 4e-6 and 65504; beyond,
 // clamped, and reported by the dK/dV pass if a query keeps them). The few blocks of the first two
 // rows work longest and start first (last, they would end 15 us after the others). 60 us at
@@ -279,8 +279,9 @@ __global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_c
     return;
   }
   if (blockIdx.y == 0) {
-    __shared__ uint32_t most[THREADS / 32];
+    __shared__ uint32_t most[THREADS / 32], v_most[THREADS / 32];
     const long long chunks = a.per_head / CHUNK;
+    const int per_row = a.d / 32;  // exponents of a row: 2 or 4
     for (int item = blockIdx.x; item < a.heads * DO_PARTS; item += gridDim.x) {
       const int head = item / DO_PARTS, part = item % DO_PARTS;
       const uint4* x = static_cast<const uint4*>(a.dout) + head * chunks;
@@ -292,11 +293,23 @@ __global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_c
         m = __vmaxu2(__vmaxu2(m, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
       }
       m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-      if (lane_id() == 0) most[threadIdx.x / 32] = m;
+      uint32_t e = 0;
+      for (long long row = (long long)part * a.N / DO_PARTS + threadIdx.x; row < (long long)(part + 1) * a.N / DO_PARTS;
+           row += THREADS) {
+        if (a.col_cnt[(long long)head * a.Tn + row / 64] <= 0) continue;
+        const uint8_t* x = a.v.exps + ((long long)head * a.N + row) * per_row;
+        for (int i = 0; i < per_row; ++i) e = max(e, x[i] <= 142 ? (uint32_t)x[i] : 0u);  // above: clamped
+      }
+      e = __reduce_max_sync(0xffffffffu, e);
+      if (lane_id() == 0) {
+        most[threadIdx.x / 32] = m;
+        v_most[threadIdx.x / 32] = e;
+      }
       __syncthreads();
       if (threadIdx.x < 32) {
         m = __reduce_max_sync(0xffffffffu, threadIdx.x < THREADS / 32 ? most[threadIdx.x] : 0u);
-        if (threadIdx.x == 0) a.do_most[item] = m << 16;
+        e = __reduce_max_sync(0xffffffffu, threadIdx.x < THREADS / 32 ? v_most[threadIdx.x] : 0u);
+        if (threadIdx.x == 0) a.do_most[item] = m << 16 | e;  // fp32 bits of |dO|, the exponent below them
       }
       __syncthreads();
     }
