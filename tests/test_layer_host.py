@@ -94,6 +94,7 @@ def test_rotary_spec_marshalling():
     (TypeError, dict(inv_freq=torch.ones(2, 2, dtype=torch.float64))),
     (ValueError, dict(inv_freq=torch.ones(0, dtype=torch.float64))),
     (ValueError, dict(inv_freq=torch.ones(5, dtype=torch.float64))),
+    (ValueError, dict(inv_freq=torch.ones(4, dtype=torch.float64, requires_grad=True))),
     (ValueError, dict(axes=(1, 2), positions=torch.zeros(2, 5, dtype=torch.int64))),
     (ValueError, dict(axes=(5, -1), positions=torch.zeros(2, 5, dtype=torch.int64))),
     (ValueError, dict(axes=(1, 1, 1, 1, 0), positions=torch.zeros(5, 5, dtype=torch.int64))),

@@ -22,7 +22,9 @@ every pending copy and raises.
 Workspaces are cached per (shape, device, CUDA stream) and allocated when an
 operation first needs one: calls on different streams never share scratch memory. A call that is captured into a CUDA graph gets
 workspaces of its own, from the graph's memory, and its device-side errors are not
-reported (a replay reads no status word).
+reported (a replay reads no status word). As for any torch operator, a captured backward
+pass wants leaves that no live eager graph holds (torch ends the capture with an
+exception otherwise).
 
 `sparse_attention(..., checkpoint="int8")` keeps q, k and v for the backward pass as
 8-bit checkpoints (module `checkpoint`) and nothing else of their size; the

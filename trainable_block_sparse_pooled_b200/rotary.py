@@ -111,6 +111,8 @@ def _spec(r: Rotary, B: int, N: int, d: int, device) -> tuple:
         raise ValueError(f"unknown layout {r.layout!r}: 'interleaved' or 'half'")
     if f.dtype != torch.float64 or f.dim() != 1:
         raise TypeError("inv_freq must be a float64 tensor of one dimension")
+    if f.requires_grad:
+        raise ValueError("inv_freq takes no gradient: detach it")
     pairs = f.shape[0]
     if pairs < 1 or 2 * pairs > d:
         raise ValueError(f"inv_freq has {pairs} frequencies: between 1 and d / 2 = {d // 2} are wanted")
