@@ -316,6 +316,16 @@ def _stream(torch):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def launch(call, device, *args) -> int:
+    """call(*args, the current stream of `device`), with `device` the current one."""
+    import torch
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+
+
 def on_device(device):
     """A context in which `device` is the current CUDA device (a launch goes to the current device's stream)."""
     import torch

@@ -90,14 +90,14 @@ class Packed:
 
 def _launch(call, items, dtype, device, what):
     """`items`: (Packed, tensor) pairs, at most PACK8_MAX to a launch, on the device's current stream."""
-    with b.on_device(device):
-        s = b._stream(torch)
-        for i in range(0, len(items), b.PACK8_MAX):
-            part = items[i:i + b.PACK8_MAX]
-            fields = [f for p, x in part for f in p.fields(x)]
-            rc = call(b.PACK8_TENSORS[len(part)].pack(*fields), len(part), _DTYPES[dtype], s)
-            if rc != b.OK:
-                raise b.Spa2Error(rc, what)
+    for i in range(0, len(items), b.PACK8_MAX):
+        part = items[i:i + b.PACK8_MAX]
+        fields = []
+        for p, x in part:
+            fields += p.fields(x)
+        rc = b.launch(call, device, b.PACK8_TENSORS[len(part)].pack(*fields), len(part), _DTYPES[dtype])
+        if rc != b.OK:
+            raise b.Spa2Error(rc, what)
 
 
 def pack8(*xs: torch.Tensor) -> tuple[Packed, ...]:

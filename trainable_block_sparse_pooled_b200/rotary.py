@@ -152,23 +152,25 @@ def _spec(r: Rotary, B: int, N: int, d: int, device) -> tuple:
 def _turned(spec, inverse: bool, strides, xs):
     """xs turned by the spa2_rotary_spec `spec`, each in strides of its own or (None) contiguous."""
     x = xs[0]
-    (B, _, N, d), dtype, device = x.shape, x.dtype, x.device
+    (B, _, N, d), dtype = x.shape, x.dtype
     fields, outs, keep = [], [], []
     for x, st in zip(xs, strides):
-        shape = x.shape
-        if x.stride(3) != 1 and d != 1:
+        xb, xh, xn, xe = x.stride()
+        if xe != 1 and d != 1:
             x = x.contiguous()
             keep.append(x)
+            xb, xh, xn, _ = x.stride()
         y = torch.empty_like(x, memory_format=torch.contiguous_format) if st is None else \
-            torch.empty_strided(shape, st, dtype=dtype, device=device)
+            torch.empty_strided(x.shape, st, dtype=dtype, device=x.device)
         outs.append(y)
-        if B and shape[1] and N:
-            fields += x.data_ptr(), y.data_ptr(), shape[1], *x.stride()[:3], *y.stride()[:3]
+        heads = x.shape[1]
+        if B and heads and N:
+            yb, yh, yn, _ = y.stride()
+            fields += x.data_ptr(), y.data_ptr(), heads, xb, xh, xn, yb, yh, yn
     n = len(fields) // 9
     if n:
-        with b.on_device(device):
-            rc = b.lib().spa2_rotary(b.ROTARY_TENSORS[n].pack(*fields), n, B, N, d, _DTYPES[dtype], spec, inverse,
-                                     b._stream(torch))
+        rc = b.launch(b.lib().spa2_rotary, x.device, b.ROTARY_TENSORS[n].pack(*fields), n, B, N, d, _DTYPES[dtype], spec,
+                      inverse)
         if rc != b.OK:
             raise b.Spa2Error(rc, "spa2_rotary")
     return outs
@@ -193,15 +195,15 @@ class RotaryFunction(torch.autograd.Function):
         at = [i for i, g in enumerate(grads) if g is not None and wanted[3 + i]]
         out = [None] * len(grads)
         if at:
-            r = Rotary(*ctx.saved_tensors, *ctx.r)
+            inv_freq, positions = ctx.saved_tensors
             strides, xs = [ctx.strides[i] for i in at], [grads[i] for i in at]
             if torch.is_grad_enabled():  # the gradient will be differentiated itself
-                turned = RotaryFunction.apply(r, not ctx.inverse, strides, *xs)
+                turned = RotaryFunction.apply(Rotary(inv_freq, positions, *ctx.r), not ctx.inverse, strides, *xs)
             else:
                 B, _, N, d = xs[0].shape
                 spec, f = ctx.spec, None
-                if not b.rotary_spec_points(spec, r.inv_freq, r.positions):  # copies of the saved tensors
-                    spec, f = _spec(r, B, N, d, xs[0].device)
+                if not b.rotary_spec_points(spec, inv_freq, positions):  # copies of the saved tensors
+                    spec, f = _spec(Rotary(inv_freq, positions, *ctx.r), B, N, d, xs[0].device)
                 turned = _turned(spec, not ctx.inverse, strides, xs)
             for i, g in zip(at, turned):
                 out[i] = g
