@@ -474,7 +474,8 @@ spa2_status spa2_sparse_attn_bwd(const void* q, const void* k, const void* v, co
     cc = w.tiles.csc_cnt;
     ci = w.tiles.csc_idx;
   }
-  BwdArgs a{&tq, &tk, &tv, &tdo, &tq16, &tdq, q, k, o, o_lo, dout, v, const_cast<float*>(lse), rc, ri, cc, ci, w.dvec, w.do16,
+  BwdArgs a{&tq, &tk, &tv, &tdo, &tq16, &tdq, q, k, o, o_lo, dout, v, const_cast<float*>(lse),
+            rc, ri, cc, ci, w.dvec, w.do16,
             w.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
             scale * 1.4426950408889634f, w.status, w.status + 32, g_wait_limit_ns, s.tiled ? 1 : 0,
             w.col_order};
@@ -562,9 +563,9 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
     cc = t.csc_cnt;
     ci = t.csc_idx;
   }
-  SPA2_CUDA_TRY(launch_unpack8_step(Unpack8Step{*k8, *v8, static_cast<uint32_t*>(w.k16), static_cast<uint32_t*>(w.v16),
-                                                dout, w.do_most, cc, w.col_order, s.N, d, s.TNt, w.split, s.BH, (long long)s.N * d},
-                                    st));
+  const Unpack8Step start{*k8, *v8, static_cast<uint32_t*>(w.k16), static_cast<uint32_t*>(w.v16), dout, w.do_most, cc,
+                          w.col_order, s.N, d, s.TNt, w.split, s.BH, (long long)s.N * d};
+  SPA2_CUDA_TRY(launch_unpack8_step(start, st));
   BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, nullptr, nullptr, nullptr, dout, nullptr, w.lse, rc, ri, cc, ci,
             w.b.dvec, w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
             scale * 1.4426950408889634f, status, status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.col_order,

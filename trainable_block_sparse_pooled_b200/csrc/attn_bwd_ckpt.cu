@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
                        const int8_t* __restrict__ q8, const uint8_t* __restrict__ qe, uint4* __restrict__ q16,
                        uint4* __restrict__ do16, const uint32_t* do_most, float* __restrict__ unscale,
-                       float* __restrict__ lse, float* __restrict__ dvec, const int* __restrict__ row_cnt, const int* __restrict__ row_idx,
+                       float* __restrict__ lse, float* __restrict__ dvec, const int* __restrict__ row_cnt,
+                       const int* __restrict__ row_idx,
                        int grad_f32, int N, int Tm, int Tn, float scale, float scale_log2, int* status,
                        unsigned long long wait_limit_ns) {
   constexpr int CH = D / 64;

@@ -116,7 +116,8 @@ SPA2_DEV void store_f16(uint32_t* to, const float (&f)[CHUNK], uint32_t E, bool&
 // There six blocks to an SM (40 registers) gain 3%; with ragged rows they would cost 20%, and fp32
 // chunks would spill.
 template <typename T, bool FLAT>
-__global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) pack8_kernel(const __grid_constant__ Pack8Args a) {
+__global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1)
+    pack8_kernel(const __grid_constant__ Pack8Args a) {
   pdl_trigger();
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
   const Places<FLAT> places(a);
@@ -159,7 +160,8 @@ __global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) pack8
 }
 
 template <typename T, bool FLAT>
-__global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1) unpack8_kernel(const __grid_constant__ Pack8Args a) {
+__global__ void __launch_bounds__(THREADS, FLAT && sizeof(T) == 2 ? 6 : 1)
+    unpack8_kernel(const __grid_constant__ Pack8Args a) {
   const spa2_pack8_tensor& t = a.t[blockIdx.y];
   const Places<FLAT> places(a);
   long long e[UNROLL], group;
@@ -263,11 +265,11 @@ cudaError_t launch_pack8_step(const spa2_pack8_tensor (&t)[3], void* v16, int* s
 }
 
 // What the backward on checkpoints starts from, by the row of the grid: 0 the largest |dO| of every
-// head and the largest exponent of V in the blocks that a query keeps, in DO_PARTS parts, 1 the order in which the dK/dV pass takes its columns, 2, 3 the kept
-// values of K and V as fp16 (exact where a group's largest is between 4e-6 and 65504; beyond,
-// clamped, and reported by the dK/dV pass if a query keeps them). The few blocks of the first two
-// rows work longest and start first (last, they would end 15 us after the others). 60 us at
-// [12, 32760, 128], for 404 MB: the measured copy rate.
+// head and the largest exponent of V in the blocks that a query keeps, in DO_PARTS parts, 1 the order
+// in which the dK/dV pass takes its columns, 2, 3 the kept values of K and V as fp16 (exact where a
+// group's largest is between 4e-6 and 65504; beyond, clamped, and reported by the dK/dV pass if a
+// query keeps them). The few blocks of the first two rows work longest and start first (last, they
+// would end 15 us after the others). 63 us at [12, 32760, 128], for 404 MB: the measured copy rate.
 __global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_constant__ Unpack8Step a) {
   pdl_trigger();
   if (blockIdx.y == 1) {
@@ -348,7 +350,9 @@ __global__ void __launch_bounds__(THREADS, 6) unpack8_step_kernel(const __grid_c
 cudaError_t launch_unpack8_step(const Unpack8Step& a, cudaStream_t s) {
   const long long chunks = a.heads * a.per_head / CHUNK;
   KernelTimer kt(KID_UNPACK8, s);
-  unpack8_step_kernel<<<dim3((unsigned)((chunks + PLACES - 1) / PLACES), 4), THREADS, 0, s>>>(a);
+  // short sequences: a block for each part of a head, up to four an SM (17 us with 8 blocks for 64 parts)
+  const long long blocks = std::max((chunks + PLACES - 1) / PLACES, std::min(a.heads * DO_PARTS, 592LL));
+  unpack8_step_kernel<<<dim3((unsigned)blocks, 4), THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
