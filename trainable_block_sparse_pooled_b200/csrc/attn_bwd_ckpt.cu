@@ -288,6 +288,10 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const long long row = (long long)i * 128 + r;
     const bool rvalid = row < N;
+    // do_most is written by the kernel before: waited for, and loaded as volatile (the compiler may move
+    // a plain load of read-only memory above the wait)
+    pdl_wait();
+    const uint32_t most = reinterpret_cast<const volatile uint32_t*>(do_most)[(long long)bh * DO_PARTS + lane];
     // Q_i from its codes into shared memory, and its fp16 copy
     bool bad = false;
 #pragma unroll
@@ -301,8 +305,13 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
         float f[4];
         pack8_floats(in[e], f);
         // codes of rows behind the last are 0, which the conversion takes for +0
-        w[2 * e] = pack_f16_clamped(f[0] * step, f[1] * step, bad);
-        w[2 * e + 1] = pack_f16_clamped(f[2] * step, f[3] * step, bad);
+        if (E[x] <= 142) {  // below 2^16: at most 65024
+          w[2 * e] = pack_f16(f[0] * step, f[1] * step);
+          w[2 * e + 1] = pack_f16(f[2] * step, f[3] * step);
+        } else {
+          w[2 * e] = pack_f16_clamped(f[0] * step, f[1] * step, bad);
+          w[2 * e + 1] = pack_f16_clamped(f[2] * step, f[3] * step, bad);
+        }
       }
       const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
       uint8_t* chunk = sm.q[c >> 2];
@@ -316,17 +325,14 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     }
     fence_proxy_async_smem();
     mbar_arrive(&sm.q_ready);
-    // do_most is written by the kernel before: waited for, and loaded as volatile (the compiler may move
-    // a plain load of read-only memory above the wait)
-    pdl_wait();
-    const uint32_t most = reinterpret_cast<const volatile uint32_t*>(do_most)[(long long)bh * DO_PARTS + lane];
     // The power of two that brings the head's largest |dO|, 2^(E - 127) or more, into [4, 8): its
     // exponent field is 127 + 129 - E (for infinities and NaN, which are reported, and zeros any will
     // do). With |V| < 2^(F - 126), F its largest exponent, |dP - D| < d 2^(F - 122) then, and where that
     // could pass 2^15 dO is scaled down further, so that dS stays within fp16's range.
     const int v_e = (int)__reduce_max_sync(0xffffffffu, most & 0xffffu);
     const uint32_t down = (uint32_t)max(0, v_e - 137 + (D == 128 ? 7 : 6));
-    const uint32_t most_e = min(max(__reduce_max_sync(0xffffffffu, most) >> 23, 29u) + down, 227u);
+    const uint32_t do_e = __reduce_max_sync(0xffffffffu, most) >> 23;
+    const uint32_t most_e = min(max(do_e, 29u) + down, 227u);
     const float do_scale = __uint_as_float((256u - most_e) << 23);
     const float back = __uint_as_float((most_e - 2u) << 23);  // its inverse
     if (i == 0 && threadIdx.x == 0) unscale[bh] = back;
@@ -338,7 +344,8 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
         uint4* at = reinterpret_cast<uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7));
         auto to16 = [&](uint32_t w) {
           const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-          return pack_f16_clamped(f.x * do_scale, f.y * do_scale, bad);
+          return do_e <= 227u ? pack_f16(f.x * do_scale, f.y * do_scale)  // below 8
+                              : pack_f16_clamped(f.x * do_scale, f.y * do_scale, bad);
         };
         const uint4 in = *at, out = make_uint4(to16(in.x), to16(in.y), to16(in.z), to16(in.w));
         *at = out;
