@@ -545,10 +545,10 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)d);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = grad_dtype == SPA2_DTYPE_F32;
-  CUtensorMap tk, tv, tdo, tdob, tq16, tdq;
+  CUtensorMap tk, tv, tdo, tq16, tdq;
   if (!make_map(&tk, w.k16, s, 64, true) || !make_map(&tv, w.v16, s, 64, true) ||
       !make_map(&tdo, w.b.do16, s, 128, true) ||
-      !make_map(&tdob, dout, s, 128) || !make_map(&tq16, w.b.q16, s, 128, true) ||
+      !make_map(&tq16, w.b.q16, s, 128, true) ||
       !(f32 ? make_map_f32(&tdq, dq, s, 128) : make_map(&tdq, dq, s, 128)))
     return SPA2_ERR_CUDA;
   int* status = w.b.status;
@@ -569,7 +569,7 @@ spa2_status spa2_sparse_attn_bwd_ckpt(const spa2_pack8_tensor* q8, const spa2_pa
   BwdArgs a{nullptr, &tk, &tv, &tdo, &tq16, &tdq, nullptr, nullptr, nullptr, nullptr, dout, nullptr, w.lse, rc, ri, cc, ci,
             w.b.dvec, w.b.do16, w.b.q16, dq, dk, dv, f32 ? 1 : 0, (int)s.BH, s.N, s.TMt, s.TNt, scale,
             scale * 1.4426950408889634f, status, status + 32, g_wait_limit_ns, s.tiled ? 1 : 0, w.col_order,
-            q8->codes, q8->exps, k8->exps, v8->exps, &tdob, w.do_most, w.unscale, w.split};
+            q8->codes, q8->exps, k8->exps, v8->exps, w.do_most, w.unscale, w.split};
   SPA2_CUDA_TRY(launch_bwd(a, d, st));
   return SPA2_OK;
 }

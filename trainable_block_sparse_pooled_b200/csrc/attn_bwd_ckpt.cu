@@ -9,8 +9,8 @@
 //             D = rowsum(dO * O) = sum_j P_ij dP_ij. The output O is never formed: no P V
 //             product, nothing of its size written or read.
 //     second  S and dP again, dS = P * (dP - D), dQ_i += dS K_j * scale.
-//   Q_i is decoded from its codes into shared memory, dO_i, K_j and V_j arrive by TMA. The fp16
-//   copies of Q and dO that the dK/dV pass streams are written from here as well.
+//   Q_i is decoded from its codes and dO_i scaled on their way into shared memory; K_j and V_j
+//   arrive by TMA. The fp16 copies of Q and dO that the dK/dV pass streams are written here too.
 //
 // Precision: every product takes fp16 operands and adds up in fp32, in this pass as in the dK/dV
 // pass. The kept values have 7 bits and are exact in fp16 (a group whose largest magnitude is
@@ -27,7 +27,7 @@
 // this one's start and end. That fixes the layout: 256 columns of tensor memory and 113 KB
 // of shared memory each, hence Q and dO in shared memory (SS products, bound by the 128
 // bytes a cycle that the tensor core reads there), K double-buffered and V single. At
-// [12, 32760, 128] with 25.6 of 512 blocks kept: 848 us; the products' shared-memory and tensor
+// [12, 32760, 128] with 25.6 of 512 blocks kept: 830 us; the products' shared-memory and tensor
 // cycles alone (768 a tile in the first pass, 1024 in the second, 531 tiles an SM) would take 560 us
 // at the 1.7 GHz that the power limit leaves. Measured and not kept: one CTA an SM with Q and dO in
 // tensor memory (as bwd_dq_kernel) 1000 us, that with 16 warps 1064; here, Q and dO in tensor memory
@@ -49,12 +49,12 @@ constexpr int DQC_THREADS = 320;  // S / dP / dS x 8 warps, TMA, MMA
 template <int D>
 struct DqcSmem {
   static constexpr int CH = D / 64;
-  // Q_i and dO_i fp16 (dO_i lands as bf16); at the end the staged dQ tile (64 KB in fp32 at d = 128)
+  // Q_i and dO_i fp16; at the end the staged dQ tile (64 KB in fp32 at d = 128)
   alignas(1024) uint8_t q[CH][128 * 128];
   alignas(1024) uint8_t dO[CH][128 * 128];
   alignas(1024) uint8_t k[2][CH][64 * 128];
   alignas(1024) uint8_t v[CH][64 * 128];
-  uint64_t q_ready, do_full, do_ready;
+  uint64_t q_ready, do_ready;
   uint64_t k_full[2], k_empty[2], v_full, v_empty;
   uint64_t sdp_full, read, ds_full;  // S and dP there; read out; dS there
   uint64_t acc_done, drain;
@@ -75,8 +75,8 @@ SPA2_DEV bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
 // dP 64..127, dQ 128 .. 128+d (between the passes: what the two halves of a row exchange).
 template <int D, bool TILED>
 __global__ void __launch_bounds__(DQC_THREADS, 2)
-    bwd_dq_ckpt_kernel(const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_dq,
+    bwd_dq_ckpt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_dq, const __nv_bfloat16* __restrict__ dout,
                        const int8_t* __restrict__ q8, const uint8_t* __restrict__ qe, uint4* __restrict__ q16,
                        uint4* __restrict__ do16, const uint32_t* do_most, float* __restrict__ unscale,
                        float* __restrict__ lse, float* __restrict__ dvec, const int* __restrict__ row_cnt,
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   constexpr int CH = D / 64;
   constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64, false, false, /*f16=*/true);
   constexpr uint32_t IDESC_Q = idesc_bf16_f32(128, D, false, true, /*f16=*/true);
-  constexpr uint32_t KV_BYTES = 64 * D * 2, ROW_BYTES = 128 * D * 2;
+  constexpr uint32_t KV_BYTES = 64 * D * 2;
   constexpr uint32_t T_S = 0, T_DP = 64, T_DQ = 128;
   constexpr float LN2 = 0.69314718055994530942f;
 
@@ -105,11 +105,13 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   const long long rowid = (long long)bh * Tm + i;
 
   // what the start waits for, asked for at once: the row's count and first block, and (warps
-  // 0-7) Q_i's codes, 16 elements of a row at a time, neighbours in neighbouring threads
-  constexpr int PER_ROW = D / 16, PIECES = 128 * PER_ROW / 256;
+  // 0-7) Q_i's codes, 16 elements of a row at a time, and dO_i, 8 at a time, neighbours in
+  // neighbouring threads
+  constexpr int PER_ROW = D / 16, PIECES = 128 * PER_ROW / 256, DO_PIECES = 2 * PIECES;
   const int count = row_cnt[rowid], first = row_idx[rowid * Tn];
   uint4 code[PIECES];
   uint8_t E[PIECES];
+  uint4 do_in[DO_PIECES];
   if (warp < 8) {
 #pragma unroll
     for (int x = 0; x < PIECES; ++x) {
@@ -119,6 +121,12 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       code[x] = there ? reinterpret_cast<const uint4*>(q8 + at * D)[c] : make_uint4(0, 0, 0, 0);
       E[x] = there ? qe[at * (D / 32) + (c >> 1)] : (uint8_t)0;
     }
+#pragma unroll
+    for (int x = 0; x < DO_PIECES; ++x) {
+      const int piece = x * 256 + threadIdx.x, pr = piece / (D / 8), c = piece % (D / 8);
+      const long long at = (long long)bh * N + (long long)i * 128 + pr;
+      do_in[x] = i * 128 + pr < N ? reinterpret_cast<const uint4*>(dout + at * D)[c] : make_uint4(0, 0, 0, 0);
+    }
   }
 
   if (warp == 9) {
@@ -127,7 +135,6 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   }
   if (threadIdx.x == 256) {
     mbar_init(&sm.q_ready, 256);
-    mbar_init(&sm.do_full, 1);
     mbar_init(&sm.do_ready, 256);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.k_full[s], 1);
@@ -160,11 +167,10 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   int epi_ok = 1;  // a dS thread clears it when its part of the dQ tile was not staged
 
   if (warp == 8) {
-    // ---------------- TMA producer: dO, then K and V of 2n tiles ----------------
+    // ---------------- TMA producer: K and V of 2n tiles ----------------
     if (lane == 0 && n > 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      tma_prefetch_desc(&tm_do);
       const int end = 2 * n;
       pdl_wait();  // K and V are decoded by the kernel before
       int kt = 0, vt = 0;  // tiles whose K, whose V has been started
@@ -181,10 +187,6 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
           }
           mbar_expect_tx(&sm.k_full[kt & 1], KV_BYTES);
           for (int c = 0; c < CH; ++c) tma_load_3d(sm.k[kt & 1][c], &tm_k, &sm.k_full[kt & 1], c * 64, j * 64, bh);
-          if (kt == 0) {
-            mbar_expect_tx(&sm.do_full, ROW_BYTES);
-            for (int c = 0; c < CH; ++c) tma_load_3d(sm.dO[c], &tm_do, &sm.do_full, c * 64, i * 128, bh);
-          }
           ++kt;
         } else if (vt < kt && (vt < 1 || mbar_test_wait(&sm.v_empty, (vt - 1) & 1))) {
           const int j = (vt == 0 ? first : kv_list[vt < n ? vt : vt - n]) & TILE_ID_MASK;
@@ -215,7 +217,6 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       // never leave with copies in flight: wait (bounded) for the last loads
       for (int t = max(0, kt - 2); t < kt; ++t) wait_bar(&sm.k_full[t & 1], (t >> 1) & 1, drain_wc);
       if (vt > 0) wait_bar(&sm.v_full, (vt - 1) & 1, drain_wc);
-      if (kt > 0) wait_bar(&sm.do_full, 0, drain_wc);
     }
   } else if (warp == 9) {
     // ---------------- MMA issuer (all 32 lanes; elect.sync picks the issuing lane) ----------------
@@ -336,24 +337,21 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     const float do_scale = __uint_as_float((256u - most_e) << 23);
     const float back = __uint_as_float((most_e - 2u) << 23);  // its inverse
     if (i == 0 && threadIdx.x == 0) unscale[bh] = back;
-    // dO_i to fp16 in place, 8 elements of a row at a time, and its copy
-    if (n > 0 && wait_warp(&sm.do_full, 0, wc)) {
+    // dO_i to fp16, and its copy
 #pragma unroll
-      for (int x = 0; x < 128 * D / 8 / 256; ++x) {
-        const int piece = x * 256 + threadIdx.x, pr = piece / (D / 8), c = piece % (D / 8);
-        uint4* at = reinterpret_cast<uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7));
-        auto to16 = [&](uint32_t w) {
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-          return do_e <= 227u ? pack_f16(f.x * do_scale, f.y * do_scale)  // below 8
-                              : pack_f16_clamped(f.x * do_scale, f.y * do_scale, bad);
-        };
-        const uint4 in = *at, out = make_uint4(to16(in.x), to16(in.y), to16(in.z), to16(in.w));
-        *at = out;
-        if (i * 128 + pr < N) do16[(((long long)bh * N + (long long)i * 128 + pr) * D) / 8 + c] = out;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.do_ready);
+    for (int x = 0; x < DO_PIECES; ++x) {
+      const int piece = x * 256 + threadIdx.x, pr = piece / (D / 8), c = piece % (D / 8);
+      auto to16 = [&](uint32_t w) {
+        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+        return do_e <= 227u ? pack_f16(f.x * do_scale, f.y * do_scale)  // below 8
+                            : pack_f16_clamped(f.x * do_scale, f.y * do_scale, bad);
+      };
+      const uint4 out = make_uint4(to16(do_in[x].x), to16(do_in[x].y), to16(do_in[x].z), to16(do_in[x].w));
+      *reinterpret_cast<uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7)) = out;
+      if (i * 128 + pr < N) do16[(((long long)bh * N + (long long)i * 128 + pr) * D) / 8 + c] = out;
     }
+    fence_proxy_async_smem();
+    mbar_arrive(&sm.do_ready);
     if (bad) report(status, SPA2_ERR_RANGE);
     const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
     // only kv-block Tn-1 (last in the ascending list) is ragged
@@ -544,8 +542,8 @@ static cudaError_t launch_dq_ckpt_t(const BwdArgs& a, cudaStream_t s) {
                                              (int)smem);
   if (e != cudaSuccess) return e;
   KernelTimer kt(KID_BWD_DQ_CKPT, s);
-  return launch_k(bwd_dq_ckpt_kernel<D, TILED>, dim3(a.Tm, a.BH), dim3(DQC_THREADS), smem, s, true, *a.tm_dob, *a.tm_k,
-                  *a.tm_v, *a.tm_dq, a.q8, a.qe, static_cast<uint4*>(a.q16), static_cast<uint4*>(a.do16), a.do_most,
+  return launch_k(bwd_dq_ckpt_kernel<D, TILED>, dim3(a.Tm, a.BH), dim3(DQC_THREADS), smem, s, true, *a.tm_k,
+                  *a.tm_v, *a.tm_dq, static_cast<const __nv_bfloat16*>(a.dout), a.q8, a.qe, static_cast<uint4*>(a.q16), static_cast<uint4*>(a.do16), a.do_most,
                   a.unscale, a.lse, a.dvec, a.row_cnt, a.row_idx, a.grad_f32, a.N, a.Tm, a.Tn, a.scale, a.scale_log2,
                   a.status, a.wait_limit_ns);
 }

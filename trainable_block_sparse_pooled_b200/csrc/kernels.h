@@ -130,7 +130,6 @@ struct BwdArgs {
   // and do_most are there, and the dQ pass writes lse, dvec, do16, q16 and unscale
   const int8_t* q8;
   const uint8_t *qe, *ke, *ve;
-  const CUtensorMap* tm_dob;  // dO bf16, box {64, 128, 1}
   const uint32_t* do_most;    // [BH, DO_PARTS]
   float* unscale;             // [BH]: do16 and dvec are dO and D divided by this power of two
   ColumnSplit split;
