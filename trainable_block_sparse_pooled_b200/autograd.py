@@ -186,18 +186,28 @@ class CheckpointedAttentionFunction(torch.autograd.Function):
         o, kept = s.fwd_ckpt(q, k, v, mask, scale)
         s.watch.after((b.OP_FWD,))
         ctx.save_for_backward(kept[0].base)
-        ctx.mask, ctx.scale, ctx.blocks = mask, scale, (bq, bkv)
+        ctx.mask, ctx.scale, ctx.spa = mask, scale, s
         return o
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, do):
-        shape, dtype = do.shape, do.dtype
-        s = _spa(*shape, do.device, *ctx.blocks)
-        kept = Packed.several_in(ctx.saved_tensors[0], shape, dtype, 3)
-        grads = s.bwd_ckpt(kept, do.contiguous(), ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
-        s.watch.after((b.OP_BWD_CKPT,))
-        return (*grads, None, None, None, None)
+        if torch.is_grad_enabled():  # wanted as a part of a graph, which cannot be differentiated again
+            return _checkpointed_backward_in_graph(ctx, do)
+        return _checkpointed_backward(ctx, do)
+
+
+def _checkpointed_backward(ctx, do):
+    s = ctx.spa
+    if torch.cuda.is_current_stream_capturing():
+        s = _spa(s.B, s.H, s.N, s.d, s.device, s.bq, s.bkv)
+    s.watch.poll()
+    kept = Packed.several_in(ctx.saved_tensors[0], do.shape, do.dtype, 3)
+    grads = s.bwd_ckpt(kept, do.contiguous(), ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
+    s.watch.after((b.OP_BWD_CKPT,))
+    return (*grads, None, None, None, None)
+
+
+_checkpointed_backward_in_graph = torch.autograd.function.once_differentiable(_checkpointed_backward)
 
 
 def _check_attention(q, k, v, mask, bq, bkv):

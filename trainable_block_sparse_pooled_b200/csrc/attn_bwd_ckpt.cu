@@ -17,10 +17,9 @@
 // below 4e-6 loses up to 2^-25; above 65504 is clamped and reported). dO is multiplied by a power
 // of two per head that brings the head's largest |dO| into [4, 8) (lower where V is above 16: dS must
 // not leave fp16's range; gradients are linear in dO, and the loss's scale must not decide what is
-// left of them), which leaves its 8 bits exact down to 2^-19 of
-// the largest. dS, formed in fp32, is rounded to 11 bits, as the dK/dV pass rounds it: relative to
-// dQ's norm 2e-4 in random rows and 8e-4 with sink keys of 8x norm, whose terms cancel, against
-// 1.65e-3 of bf16 gradients.
+// left of them), which leaves its 8 bits exact down to 2^-19 of the largest. dS, formed in fp32, is
+// rounded to 11 bits, as the dK/dV pass rounds it: relative to dQ's norm 2e-4 in random rows and 8e-4
+// with sink keys of 8x norm, whose terms cancel, against 1.65e-3 of bf16 gradients.
 //
 // What bounds it: each product chain of a CTA is serial (S and dP have one buffer each, dS
 // goes over S), so a second CTA on the SM works through its own chain meanwhile, and through
