@@ -260,6 +260,18 @@ def test_only_8_bits_are_kept_and_a_second_backward_is_refused():
         loss.backward()
 
 
+def test_a_second_derivative_is_refused():
+    """create_graph gives the same gradients; differentiating them again raises."""
+    q, k, v = (x.requires_grad_() for x in synth.gaussian_with_sinks(B=1, H=1, N=300, d=64, seed=27, device="cuda"))
+    m = block_mask(q.detach(), k.detach(), 0.3, 0.5)
+    dout = synth.normal_like(q.shape, seed=28, device="cuda").requires_grad_()
+    o = sparse_attention(q, k, v, mask=m, checkpoint="int8")
+    grads = torch.autograd.grad(o, (q, k, v), dout, create_graph=True)
+    assert all(torch.equal(a, w) for a, w in zip(grads, attention(q, k, v, dout.detach(), m)[1:]))
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(grads[0].float().sum(), q)
+
+
 def test_no_gradient_keeps_nothing():
     q, k, v = synth.gaussian_with_sinks(B=1, H=1, N=300, d=64, seed=2, device="cuda")
     m = block_mask(q, k, 0.3, 0.5)
