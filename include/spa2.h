@@ -333,7 +333,7 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
  * writes dQ, dK, dV: the gradients of the attention at the kept values. Products
  * take fp16 operands and add up in fp32: the kept values (exact where a group's
  * largest magnitude is between 4e-6 and 65504; beyond, clamped and reported as
- * SPA2_ERR_RANGE), P and dS (11 bits each), and dO times a power of two per head
+ * SPA2_ERR_RANGE), P and dS (11 bits each; in dQ = dS K dS is a pair of halves, 22 bits), and dO times a power of two per head
  * that brings the head's largest |dO| into [4, 8), lower where |V| is above 16 (so
  * that dS stays in range): gradients of any size keep their precision (infinities
  * and NaN are reported as SPA2_ERR_RANGE).

@@ -17,9 +17,10 @@
 // below 4e-6 loses up to 2^-25; above 65504 is clamped and reported). dO is multiplied by a power
 // of two per head that brings the head's largest |dO| into [4, 8) (lower where V is above 16: dS must
 // not leave fp16's range; gradients are linear in dO, and the loss's scale must not decide what is
-// left of them), which leaves its 8 bits exact down to 2^-19 of the largest. dS, formed in fp32, is
-// rounded to 11 bits, as the dK/dV pass rounds it: relative to dQ's norm 2e-4 in random rows and 8e-4
-// with sink keys of 8x norm, whose terms cancel, against 1.65e-3 of bf16 gradients.
+// left of them), which leaves its 8 bits exact down to 2^-19 of the largest. dS, formed in fp32, enters
+// dQ = dS K as a pair of halves, 22 bits (bwd_dq_kernel: a pair of bf16). A single half is off by 7e-4 of
+// dQ's norm with sink keys of 8x norm, whose terms cancel, and by up to 1.7e-2 in places, of the 2e-2 that is
+// promised; the pair by 3e-6 and 1.2e-4 ([12, 8192, 128]). It costs four products a tile, 4% of the step.
 //
 // What bounds it: each product chain of a CTA is serial (S and dP have one buffer each, dS
 // goes over S), so a second CTA on the SM works through its own chain meanwhile, and through
@@ -70,8 +71,8 @@ SPA2_DEV bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
 
 }  // namespace
 
-// TMEM columns: S 0..63 (dS of kv columns 32h .. 32h+31 over 32h .. 32h+15),
-// dP 64..127, dQ 128 .. 128+d (between the passes: what the two halves of a row exchange).
+// TMEM columns: S 0..63 (over 16 kv columns of it their dS: the high halves in the first 8, the low ones in the
+// other 8), dP 64..127, dQ 128 .. 128+d (between the passes: what the two halves of a row exchange).
 template <int D, bool TILED>
 __global__ void __launch_bounds__(DQC_THREADS, 2)
     bwd_dq_ckpt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -236,13 +237,13 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
                     sdesc_sw128(smem_u32(sm.v[kk >> 2]) + (kk & 3) * 32, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
         mma_commit_el(&sm.v_empty);
       };
-      // dQ += dS(g) K(g), K = 64 kv rows
+      // dQ += (dS_hi + dS_lo)(g) K(g), K = 64 kv rows
       auto issue_dq = [&](int g) {
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ts_el(tmem + T_DQ, tmem + T_S + (kk >> 1) * 32 + (kk & 1) * 8,
-                    sdesc_sw128(smem_u32(sm.k[g & 1][0]) + kk * 2048, 64 * 128, 1024), IDESC_Q,
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_el(tmem + T_DQ, tmem + T_S + kk * 8,
+                    sdesc_sw128(smem_u32(sm.k[g & 1][0]) + (kk >> 1) * 2048, 64 * 128, 1024), IDESC_Q,
                     (g > n || kk > 0) ? 1u : 0u);
         mma_commit_el(&sm.k_empty[g & 1]);
       };
@@ -450,11 +451,10 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&sm.read);  // dP may be overwritten
-      uint32_t ds[16];
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
         const int c0 = h * 32 + sub * 16;
-        uint32_t sa[16];
+        uint32_t sa[16], ds[16];
         tmem_ld16(tl + T_S + c0, sa);
         tmem_wait_ld();
 #pragma unroll
@@ -471,10 +471,12 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
               f2_sub(f2_pack(__uint_as_float(pa[sub * 16 + 2 * e]), __uint_as_float(pa[sub * 16 + 2 * e + 1])), d2));
           float s0, s1;
           f2_unpack(ds2, s0, s1);
-          ds[sub * 8 + e] = pack_f16(s0, s1);
+          ds[e] = pack_f16(s0, s1);
+          const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&ds[e]));
+          ds[8 + e] = pack_f16(s0 - hi.x, s1 - hi.y);
         }
+        tmem_st16(tl + T_S + c0, ds);  // over these columns of S (read by this warp alone)
       }
-      tmem_st16(tl + T_S + h * 32, ds);  // over these columns of S (read by this warp alone)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sm.ds_full);
