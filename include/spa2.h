@@ -333,10 +333,12 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
  * writes dQ, dK, dV: the gradients of the attention at the kept values. Products
  * take fp16 operands and add up in fp32: the kept values (exact where a group's
  * largest magnitude is between 4e-6 and 65504; beyond, clamped and reported as
- * SPA2_ERR_RANGE), P and dS (11 bits each; in dQ = dS K dS is a pair of halves, 22 bits), and dO times a power of two per head
- * that brings the head's largest |dO| into [4, 8), lower where |V| is above 16 (so
- * that dS stays in range): gradients of any size keep their precision (infinities
- * and NaN are reported as SPA2_ERR_RANGE).
+ * SPA2_ERR_RANGE), P and dS (11 bits each; in dQ = dS K dS is a pair of halves, 22 bits), and dO times a power of two
+ * that brings the largest |dO| into [4, 8), lower where |V| is above 16 (so that dS
+ * stays in range): the row's largest for dQ, so that every row of dQ has its full precision;
+ * the head's largest for dK and dV, whose precision is relative to it (an element of dO,
+ * or a dS, below 2^-17 of it loses bits, below 2^-27 everything). Infinities and NaN
+ * are reported as SPA2_ERR_RANGE.
  * Keeping O and LSE instead of recomputing them is cheaper but not close: with q,
  * k, v rounded to 8 bits and O, LSE not, the rows of dS no longer sum to zero,
  * and sink keys of 8x norm amplify that to 12% of dQ (4% with recomputation).

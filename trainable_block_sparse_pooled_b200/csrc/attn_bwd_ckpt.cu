@@ -15,9 +15,11 @@
 // Precision: every product takes fp16 operands and adds up in fp32, in this pass as in the dK/dV
 // pass. The kept values have 7 bits and are exact in fp16 (a group whose largest magnitude is
 // below 4e-6 loses up to 2^-25; above 65504 is clamped and reported). dO is multiplied by a power
-// of two per head that brings the head's largest |dO| into [4, 8) (lower where V is above 16: dS must
-// not leave fp16's range; gradients are linear in dO, and the loss's scale must not decide what is
-// left of them), which leaves its 8 bits exact down to 2^-19 of the largest. dS, formed in fp32, enters
+// of two that brings the largest |dO| into [4, 8) (lower where V is above 16: dS must not leave fp16's
+// range; gradients are linear in dO, and the loss's scale must not decide what is left of them), which
+// leaves its 8 bits exact down to 2^-19 of the largest. Here that is the row's largest, since a row of dQ depends on
+// no other row of dO; in the dK/dV pass, whose sums run over the rows, it is the head's. With the head's
+// factor alone a row of 2^-12 of the largest would lose 4e-3 of its dQ, one of 2^-16 9e-2. dS, formed in fp32, enters
 // dQ = dS K as a pair of halves, 22 bits (bwd_dq_kernel: a pair of bf16). A single half is off by 7e-4 of
 // dQ's norm with sink keys of 8x norm, whose terms cancel, and by up to 1.7e-2 in places, of the 2e-2 that is
 // promised; the pair by 3e-6 and 1.2e-4 ([12, 8192, 128]). It costs four products a tile, 4% of the step.
@@ -61,6 +63,7 @@ struct DqcSmem {
   uint32_t tmem_base;
   int abort_flag;
   int never;  // stays 0: abort flag of the teardown drains
+  uint8_t row_e[128];  // exponent that a row's factor stands for
 };
 static_assert(2 * (sizeof(DqcSmem<128>) + 1024) <= 228 * 1024, "two CTAs share an SM");
 
@@ -326,29 +329,38 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     }
     fence_proxy_async_smem();
     mbar_arrive(&sm.q_ready);
-    // The power of two that brings the head's largest |dO|, 2^(E - 127) or more, into [4, 8): its
-    // exponent field is 127 + 129 - E (for infinities and NaN, which are reported, and zeros any will
-    // do). With |V| < 2^(F - 126), F its largest exponent, |dP - D| < d 2^(F - 122) then, and where that
-    // could pass 2^15 dO is scaled down further, so that dS stays within fp16's range.
+    // The power of two that brings the largest |dO|, of a row for this pass and of the head for the dK/dV
+    // pass, 2^(E - 127) or more, into [4, 8): its exponent field is 127 + 129 - E (for infinities and NaN,
+    // which are reported, and zeros any will do). With |V| < 2^(F - 126), F its largest exponent, |dP - D| <
+    // d 2^(F - 122) then, and where that could pass 2^15 dO is scaled down further, so that dS stays within
+    // fp16's range.
     const int v_e = (int)__reduce_max_sync(0xffffffffu, most & 0xffffu);
     const uint32_t down = (uint32_t)max(0, v_e - 137 + (D == 128 ? 7 : 6));
-    const uint32_t do_e = __reduce_max_sync(0xffffffffu, most) >> 23;
-    const uint32_t most_e = min(max(do_e, 29u) + down, 227u);
+    auto factor_e = [&](uint32_t e) { return min(max(e, 29u) + down, 227u); };
+    const uint32_t do_e = __reduce_max_sync(0xffffffffu, most) >> 23, most_e = factor_e(do_e);
     const float do_scale = __uint_as_float((256u - most_e) << 23);
-    const float back = __uint_as_float((most_e - 2u) << 23);  // its inverse
-    if (i == 0 && threadIdx.x == 0) unscale[bh] = back;
-    // dO_i to fp16, and its copy
+    if (i == 0 && threadIdx.x == 0) unscale[bh] = __uint_as_float((most_e - 2u) << 23);  // its inverse
+    // dO_i to fp16, by its row's factor, and a copy by the head's
 #pragma unroll
     for (int x = 0; x < DO_PIECES; ++x) {
       const int piece = x * 256 + threadIdx.x, pr = piece / (D / 8), c = piece % (D / 8);
-      auto to16 = [&](uint32_t w) {
+      const uint4 in = do_in[x];
+      uint32_t m = __vmaxu2(__vmaxu2(in.x & 0x7fff7fffu, in.y & 0x7fff7fffu),
+                            __vmaxu2(in.z & 0x7fff7fffu, in.w & 0x7fff7fffu));
+      m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t row_e = factor_e(m >> 7);
+      if (c == 0) sm.row_e[pr] = (uint8_t)row_e;
+      auto to16 = [&](uint32_t w, float by) {
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-        return do_e <= 227u ? pack_f16(f.x * do_scale, f.y * do_scale)  // below 8
-                            : pack_f16_clamped(f.x * do_scale, f.y * do_scale, bad);
+        return do_e <= 227u ? pack_f16(f.x * by, f.y * by)  // below 8
+                            : pack_f16_clamped(f.x * by, f.y * by, bad);
       };
-      const uint4 out = make_uint4(to16(do_in[x].x), to16(do_in[x].y), to16(do_in[x].z), to16(do_in[x].w));
-      *reinterpret_cast<uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7)) = out;
-      if (i * 128 + pr < N) do16[(((long long)bh * N + (long long)i * 128 + pr) * D) / 8 + c] = out;
+      auto all16 = [&](float by) { return make_uint4(to16(in.x, by), to16(in.y, by), to16(in.z, by), to16(in.w, by)); };
+      *reinterpret_cast<uint4*>(sm.dO[c >> 3] + sw128_offset(pr, c & 7)) =
+          all16(__uint_as_float((256u - row_e) << 23));
+      if (i * 128 + pr < N) do16[(((long long)bh * N + (long long)i * 128 + pr) * D) / 8 + c] = all16(do_scale);
     }
     fence_proxy_async_smem();
     mbar_arrive(&sm.do_ready);
@@ -402,7 +414,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       l = l2[0] + l2[1];
       wsum = w2[0] + w2[1];
     }
-    float nlse2 = -INFINITY, Dr = 0.f;
+    float nlse2 = -INFINITY, Dr = 0.f, back = 0.f;
     if (n > 0) {
       // the two halves of a row meet in the dQ columns, which nothing uses yet
       {
@@ -427,9 +439,11 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
           Dr = (w0 + w1) / l;
         }
       }
+      const uint32_t row_e = sm.row_e[r], below = most_e - row_e;
+      back = __uint_as_float((row_e - 2u) << 23);
       if (h == 0 && rvalid && ok) {  // +inf: a row that keeps nothing, as the dK/dV pass takes it
         lse[(long long)bh * N + row] = -nlse2 * LN2;
-        dvec[(long long)bh * N + row] = Dr;
+        dvec[(long long)bh * N + row] = below < 127u ? Dr * __uint_as_float((127u - below) << 23) : 0.f;
       }
       if (!rvalid) {
         nlse2 = -INFINITY;
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       tc_fence_before();
       mbar_arrive(&sm.ds_full);
     }
-    // epilogue: dQ_i = scale * acc without dO's factor, warpgroup h holding feature columns h*D/2 .. +D/2, staged in
+    // epilogue: dQ_i = scale * acc without the row's factor, warpgroup h holding feature columns h*D/2 .. +D/2, staged in
     // the space of Q and dO (every product is done) as 128-byte-swizzled boxes of 128 rows x 128
     // bytes (32 fp32 or 64 bf16 columns) for the TMA stores below; the tensor map clips the rows
     // of a ragged last q-block
