@@ -337,8 +337,9 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
  * that brings the largest |dO| into [4, 8), lower where |V| is above 16 (so that dS
  * stays in range): the row's largest for dQ, so that every row of dQ has its full precision;
  * the head's largest for dK and dV, whose precision is relative to it (an element of dO,
- * or a dS, below 2^-17 of it loses bits, below 2^-27 everything). Infinities and NaN
- * are reported as SPA2_ERR_RANGE.
+ * or a dS, below 2^-17 of it loses bits, below 2^-27 everything). dO may have any size that
+ * bf16 holds; infinities, NaN and what |V| above 16 takes past its range are reported as
+ * SPA2_ERR_RANGE.
  * Keeping O and LSE instead of recomputing them is cheaper but not close: with q,
  * k, v rounded to 8 bits and O, LSE not, the rows of dS no longer sum to zero,
  * and sink keys of 8x norm amplify that to 12% of dQ (4% with recomputation).

@@ -98,3 +98,22 @@ def test_query_gradients_among_sink_keys(N, d, bq, bkv):
     s = b.Spa2(1, 2, N, d, bq=bq, bkv=bkv)
     got, want = gradients(q, k, v, dout, s.block_mask(q, k, 0.2, 0.6), bq, bkv)
     assert np.abs(got[0] - want[0]).max() <= 2e-3
+
+
+@pytest.mark.parametrize("power", [-115, -100, 100, 115])
+def test_gradients_of_any_size_that_bf16_holds(power):
+    """Powers of two of dO's head come through, also near the ends of bf16's range. The elements of dO are whole
+    numbers up to 8, so that 2^-115 of them is exact in bf16 (its smallest normal number is 2^-126);
+    the results are compared in fp32, whose own steps below 2^-126 are 2^-149."""
+    q, k, v, dout = normal(300, 64, H=2, seed=3)
+    dout = dout.float().round().clamp(-8, 8).to(BF16)
+    s = b.Spa2(1, 2, 300, 64)
+    m = s.block_mask(q, k, 0.5, 0.5)
+    packed = pack8(q, k, v)
+    want = s.bwd_ckpt(packed, dout, m)
+    s.check()
+    by = torch.tensor(power, device="cuda")
+    got = s.bwd_ckpt(packed, torch.ldexp(dout.double(), by).to(BF16), m)
+    s.check()
+    for g, w in zip(got, want):
+        assert ((g.double() - torch.ldexp(w.double(), by)).abs() <= 2.0 ** -149).all()

@@ -452,22 +452,22 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_c
         tmem_ld32(tl + col, a);
         tmem_ld32(tl + col + 32, b);
         tmem_wait_ld();
-        const float f = KV16 ? (which == 0 ? back : scale * back) : which == 0 ? 1.f : scale;
+        const float f = which == 0 ? 1.f : scale;
         void* dst = which == 0 ? dv : dk;
         if (r < D) {
           if (grad_f32) {
             float* o = static_cast<float*>(dst) + base;
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              if (c < kv_valid) o[(long long)c * D] = __uint_as_float(a[c]) * f;
-              if (c + 32 < kv_valid) o[(long long)(c + 32) * D] = __uint_as_float(b[c]) * f;
+              if (c < kv_valid) o[(long long)c * D] = __uint_as_float(a[c]) * f * back;
+              if (c + 32 < kv_valid) o[(long long)(c + 32) * D] = __uint_as_float(b[c]) * f * back;
             }
           } else {
             __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dst) + base;
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              if (c < kv_valid) o[(long long)c * D] = __float2bfloat16(__uint_as_float(a[c]) * f);
-              if (c + 32 < kv_valid) o[(long long)(c + 32) * D] = __float2bfloat16(__uint_as_float(b[c]) * f);
+              if (c < kv_valid) o[(long long)c * D] = __float2bfloat16(__uint_as_float(a[c]) * f * back);
+              if (c + 32 < kv_valid) o[(long long)(c + 32) * D] = __float2bfloat16(__uint_as_float(b[c]) * f * back);
             }
           }
         }
@@ -513,9 +513,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1) bwd_dkdv_kernel(const __grid_c
           const float4 y = __ldcg(reinterpret_cast<const float4*>(place + x * (2 * SIZE) + e * (4 * D)));
           sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
         }
-        const float f = which == 0 ? back : scale * back;
+        const float f = which == 0 ? 1.f : scale;
         void* dst = which == 0 ? dv : dk;
-        const float v[4] = {sum.x * f, sum.y * f, sum.z * f, sum.w * f};
+        const float v[4] = {sum.x * f * back, sum.y * f * back, sum.z * f * back, sum.w * f * back};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (c + i >= kv_valid) continue;

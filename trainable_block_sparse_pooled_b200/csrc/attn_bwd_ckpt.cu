@@ -336,10 +336,11 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     // fp16's range.
     const int v_e = (int)__reduce_max_sync(0xffffffffu, most & 0xffffu);
     const uint32_t down = (uint32_t)max(0, v_e - 137 + (D == 128 ? 7 : 6));
-    auto factor_e = [&](uint32_t e) { return min(max(e, 29u) + down, 227u); };
+    auto factor_e = [&](uint32_t e) { return min(max(e, 3u) + down, 255u); };
     const uint32_t do_e = __reduce_max_sync(0xffffffffu, most) >> 23, most_e = factor_e(do_e);
     const float do_scale = __uint_as_float((256u - most_e) << 23);
     if (i == 0 && threadIdx.x == 0) unscale[bh] = __uint_as_float((most_e - 2u) << 23);  // its inverse
+    bad = bad || do_e + down > 255u;
     // dO_i to fp16, by its row's factor, and a copy by the head's
 #pragma unroll
     for (int x = 0; x < DO_PIECES; ++x) {
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       if (c == 0) sm.row_e[pr] = (uint8_t)row_e;
       auto to16 = [&](uint32_t w, float by) {
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-        return do_e <= 227u ? pack_f16(f.x * by, f.y * by)  // below 8
+        return do_e <= 254u ? pack_f16(f.x * by, f.y * by)  // below 8
                             : pack_f16_clamped(f.x * by, f.y * by, bad);
       };
       auto all16 = [&](float by) { return make_uint4(to16(in.x, by), to16(in.y, by), to16(in.z, by), to16(in.w, by)); };
@@ -502,7 +503,8 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     if (ok) ok = wait_warp(&sm.acc_done, 0, wc);
     if (ok) {
       tc_fence_after();
-      const float f = scale * back;
+      // scale first: times a far power of two it might be a subnormal number
+      auto out = [&](uint32_t acc) { return __uint_as_float(acc) * scale * back; };
       uint8_t* stage = &sm.q[0][0];
 #pragma unroll 1
       for (int cc = 0; cc < D / 64; ++cc) {
@@ -515,18 +517,18 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<float4*>(box + sw128_offset(r, e)) =
-                make_float4(__uint_as_float(a[4 * e]) * f, __uint_as_float(a[4 * e + 1]) * f,
-                            __uint_as_float(a[4 * e + 2]) * f, __uint_as_float(a[4 * e + 3]) * f);
+                make_float4(out(a[4 * e]), out(a[4 * e + 1]),
+                            out(a[4 * e + 2]), out(a[4 * e + 3]));
         } else {
           uint8_t* box = stage + (c0 / 64) * (128 * 128);
           const uint32_t u0 = (uint32_t)((c0 % 64) / 8);  // 16-byte unit of the slice in its 64-column box
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             *reinterpret_cast<uint4*>(box + sw128_offset(r, u0 + e)) =
-                make_uint4(pack_bf16(__uint_as_float(a[8 * e]) * f, __uint_as_float(a[8 * e + 1]) * f),
-                           pack_bf16(__uint_as_float(a[8 * e + 2]) * f, __uint_as_float(a[8 * e + 3]) * f),
-                           pack_bf16(__uint_as_float(a[8 * e + 4]) * f, __uint_as_float(a[8 * e + 5]) * f),
-                           pack_bf16(__uint_as_float(a[8 * e + 6]) * f, __uint_as_float(a[8 * e + 7]) * f));
+                make_uint4(pack_bf16(out(a[8 * e]), out(a[8 * e + 1])),
+                           pack_bf16(out(a[8 * e + 2]), out(a[8 * e + 3])),
+                           pack_bf16(out(a[8 * e + 4]), out(a[8 * e + 5])),
+                           pack_bf16(out(a[8 * e + 6]), out(a[8 * e + 7])));
         }
       }
       fence_proxy_async_smem();
