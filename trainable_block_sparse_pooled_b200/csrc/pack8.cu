@@ -216,13 +216,12 @@ __global__ void __launch_bounds__(THREADS) unpack8_single_kernel(const __grid_co
 }
 
 template <typename T>
-static cudaError_t launch_pack8_t(Pack8Args& a, int n, bool unpack, cudaStream_t s) {
+static cudaError_t launch_pack8_t(Pack8Args& a, int n, bool unpack, cudaStream_t s) {  // n >= 1 tensors, none empty
   long long groups = 0;
   bool chunks = true, flat = true;
   for (int i = 0; i < n; ++i) {
     const spa2_pack8_tensor& t = a.t[i];
     groups = std::max(groups, (long long)(t.rows * ((t.d + 31) / 32)));
-    if (t.rows == 0) continue;
     chunks &= t.d % CHUNK == 0 && t.d < (1LL << 31) && reinterpret_cast<uintptr_t>(t.x) % 16 == 0 &&
               reinterpret_cast<uintptr_t>(t.codes) % CHUNK == 0;
     flat &= t.d % SPA2_PACK8_GROUP == 0;
@@ -236,7 +235,6 @@ static cudaError_t launch_pack8_t(Pack8Args& a, int n, bool unpack, cudaStream_t
       a.div_shift[i] = l - 1;
     }
   }
-  if (groups == 0) return cudaSuccess;
   KernelTimer kt(unpack ? KID_UNPACK8 : KID_PACK8, s);
   if (chunks) {
     const dim3 grid((unsigned)((groups * PER_GROUP + PLACES - 1) / PLACES), (unsigned)n);
@@ -367,9 +365,11 @@ static spa2_status pack8_call(const spa2_pack8_tensor* t, int n, int dtype, bool
     if (t[i].rows && (!t[i].x || !t[i].codes || !t[i].exps || reinterpret_cast<uintptr_t>(t[i].x) % esz))
       return SPA2_ERR_INVALID_ARG;
   }
+  // without the empty ones, for which the kernels' division by places per row has no divisor
   Pack8Args a{};
-  std::copy(t, t + n, a.t);
-  return launch(a, n, dtype, unpack, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SPA2_OK : SPA2_ERR_CUDA;
+  const int full = (int)(std::copy_if(t, t + n, a.t, [](const spa2_pack8_tensor& x) { return x.rows > 0; }) - a.t);
+  if (full == 0) return SPA2_OK;
+  return launch(a, full, dtype, unpack, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SPA2_OK : SPA2_ERR_CUDA;
 }
 
 }  // namespace spa2
