@@ -20,8 +20,9 @@ once such a copy has landed with an error in it, and `check_errors()` waits for
 every pending copy and raises.
 
 Workspaces are cached per (shape, device, CUDA stream) and allocated when an
-operation first needs one: calls on different streams never share scratch memory. A call that is captured into a CUDA graph gets
-workspaces of its own, from the graph's memory, and its device-side errors are not
+operation first needs one: calls on different streams never share scratch memory. Host
+threads that share a stream share its workspaces; a lock keeps the launches of one
+operation together. A call that is captured into a CUDA graph gets workspaces of its own, from the graph's memory, and its device-side errors are not
 reported (a replay reads no status word). As for any torch operator, a captured backward
 pass wants leaves that no live eager graph holds (torch ends the capture with an
 exception otherwise).
@@ -34,6 +35,7 @@ gradients there. `rotary=` turns q and k by their positions first (module `rotar
 
 from __future__ import annotations
 
+import threading
 from collections import deque
 
 import torch
@@ -43,11 +45,13 @@ from .checkpoint import Packed
 from .rotary import Rotary, apply_rotary
 
 _cache: dict = {}
+_cache_lock = threading.Lock()
 
 
 class _StatusWatch:
     """Stream-ordered, non-blocking copies of one Spa2's status words into pinned memory. A
-    slot holds PENDING until its copy lands, so a look at it needs no event."""
+    slot holds PENDING until its copy lands, so a look at it needs no event. Used under the
+    Spa2's lock."""
 
     SLOTS, PENDING = 16, -1
 
@@ -108,6 +112,9 @@ class _NoWatch:
 
 
 def _spa(B, H, N, d, device, bq=b.BQ, bkv=b.BKV) -> b.Spa2:
+    """The Spa2 of this shape and the current stream. An operation on it holds its `lock` from the first launch to
+    the status copy: the kernels of one C call hand each other data through the workspace, and another thread's
+    launches on the same stream must not come between them."""
     if torch.cuda.is_current_stream_capturing():
         # graphs replay on any stream, two of them at once: each call owns its workspaces
         s = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv, lazy=True)
@@ -117,9 +124,12 @@ def _spa(B, H, N, d, device, bq=b.BQ, bkv=b.BKV) -> b.Spa2:
     key = (B, H, N, d, bq, bkv, index, torch._C._cuda_getCurrentRawStream(index))
     s = _cache.get(key)
     if s is None:
-        s = _cache[key] = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv, lazy=True)
-        s.watch = _StatusWatch(s)
-    s.watch.poll()
+        with _cache_lock:
+            s = _cache.get(key)
+            if s is None:
+                s = b.Spa2(B, H, N, d, device=device, bq=bq, bkv=bkv, lazy=True)
+                s.watch = _StatusWatch(s)
+                _cache[key] = s
     return s
 
 
@@ -128,7 +138,8 @@ def check_errors():
     `Spa2Error` if any call of sparse_attention / block_mask recorded a
     device-side error."""
     for s in list(_cache.values()):
-        s.watch.drain()
+        with s.lock:
+            s.watch.drain()
 
 
 class SparseAttentionFunction(torch.autograd.Function):
@@ -148,15 +159,18 @@ class SparseAttentionFunction(torch.autograd.Function):
         B, H, N, d = q.shape
         s = _spa(B, H, N, d, q.device, bq, bkv)
         ops = [b.OP_FWD]
-        if mask is None:
-            mask = s.block_mask(q, k, k_frac, p_frac)
-            ops.insert(0, b.OP_MASK)
-        elif tuple(mask.row_cnt.shape) != (B, H, s.Tm) or tuple(mask.row_idx.shape) != (B, H, s.Tm, s.Tn) \
-                or mask.col_cnt is None or mask.row_cnt.device != q.device:
+        if mask is not None and (tuple(mask.row_cnt.shape) != (B, H, s.Tm) or tuple(mask.row_idx.shape) != (B, H, s.Tm, s.Tn)
+                                 or mask.col_cnt is None or mask.row_cnt.device != q.device):
             raise ValueError("mask does not belong to a problem of this shape and device")
-        o, lse = s.fwd(q, k, v, mask, scale)
-        s.watch.after(ops)
-        ctx.save_for_backward(q, k, v, o, lse, s.o_lo)
+        with s.lock:
+            s.watch.poll()
+            if mask is None:
+                mask = s.block_mask(q, k, k_frac, p_frac)
+                ops.insert(0, b.OP_MASK)
+            o, lse = s.fwd(q, k, v, mask, scale)
+            o_lo = s.o_lo
+            s.watch.after(ops)
+        ctx.save_for_backward(q, k, v, o, lse, o_lo)
         ctx.mask, ctx.scale, ctx.spa = mask, scale, s
         row_cnt = mask.row_cnt.clone()  # the kept-block counts (a copy: a reused mask serves many calls)
         ctx.mark_non_differentiable(row_cnt)
@@ -168,10 +182,11 @@ class SparseAttentionFunction(torch.autograd.Function):
         spa = ctx.spa
         if torch.cuda.is_current_stream_capturing():
             spa = _spa(spa.B, spa.H, spa.N, spa.d, spa.device, spa.bq, spa.bkv)
-        spa.watch.poll()
-        dq, dk, dv = spa.bwd(q, k, v, o, lse, do.contiguous(), ctx.mask, ctx.scale, o_lo=o_lo,
-                             grad_dtype=b.DTYPE_BF16)
-        spa.watch.after([b.OP_BWD])
+        do = do.contiguous()
+        with spa.lock:
+            spa.watch.poll()
+            dq, dk, dv = spa.bwd(q, k, v, o, lse, do, ctx.mask, ctx.scale, o_lo=o_lo, grad_dtype=b.DTYPE_BF16)
+            spa.watch.after([b.OP_BWD])
         return dq, dk, dv, None, None, None, None, None, None
 
 
@@ -183,8 +198,10 @@ class CheckpointedAttentionFunction(torch.autograd.Function):
     def forward(ctx, q, k, v, scale: float, mask: b.Mask, bq: int, bkv: int):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         s = _spa(*q.shape, q.device, bq, bkv)
-        o, kept = s.fwd_ckpt(q, k, v, mask, scale)
-        s.watch.after((b.OP_FWD,))
+        with s.lock:
+            s.watch.poll()
+            o, kept = s.fwd_ckpt(q, k, v, mask, scale)
+            s.watch.after((b.OP_FWD,))
         ctx.save_for_backward(kept[0].base)
         ctx.mask, ctx.scale, ctx.spa = mask, scale, s
         return o
@@ -200,10 +217,11 @@ def _checkpointed_backward(ctx, do):
     s = ctx.spa
     if torch.cuda.is_current_stream_capturing():
         s = _spa(s.B, s.H, s.N, s.d, s.device, s.bq, s.bkv)
-    s.watch.poll()
-    kept = Packed.several_in(ctx.saved_tensors[0], do.shape, do.dtype, 3)
-    grads = s.bwd_ckpt(kept, do.contiguous(), ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
-    s.watch.after((b.OP_BWD_CKPT,))
+    kept, do = Packed.several_in(ctx.saved_tensors[0], do.shape, do.dtype, 3), do.contiguous()
+    with s.lock:
+        s.watch.poll()
+        grads = s.bwd_ckpt(kept, do, ctx.mask, ctx.scale, grad_dtype=b.DTYPE_BF16)
+        s.watch.after((b.OP_BWD_CKPT,))
     return (*grads, None, None, None, None)
 
 
@@ -237,8 +255,10 @@ def block_mask(q, k, k_frac: float, p_frac: float, bq: int = b.BQ, bkv: int = b.
     B, H, N, d = q.shape
     with b.on_device(q.device):
         s = _spa(B, H, N, d, q.device, bq, bkv)
-        m = s.block_mask(q, k, k_frac, p_frac)
-        s.watch.after([b.OP_MASK])
+        with s.lock:
+            s.watch.poll()
+            m = s.block_mask(q, k, k_frac, p_frac)
+            s.watch.after([b.OP_MASK])
     return m
 
 

@@ -16,6 +16,7 @@ import math
 import os
 import re
 import struct
+import threading
 from dataclasses import dataclass
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -355,7 +356,8 @@ class Spa2:
     Buffers (mask, workspaces, outputs) are allocated through torch by the
     caller side of the ABI; the library itself never allocates. The workspaces of
     the mask, the forward and the backward exist from the start unless `lazy`;
-    that of bwd_ckpt is allocated at its first call.
+    that of bwd_ckpt is allocated at its first call. Threads that share one hold its
+    `lock` over a call and the reading of its status.
     """
 
     def __init__(self, B, H, N, d, device="cuda", with_pbar=False, with_bitmap=False, bq=BQ, bkv=BKV, lazy=False):
@@ -374,6 +376,7 @@ class Spa2:
             # zero-filled so that the status word of an op never run reads as OK
             self.ws.update((op, torch.zeros(n, dtype=torch.uint8, device=device)) for op, n in self.ws_bytes.items())
         self.with_pbar, self.with_bitmap = with_pbar, with_bitmap
+        self.lock = threading.RLock()
 
     def new_mask(self) -> Mask:
         t, B, H, Tm, Tn = self.torch, self.B, self.H, self.Tm, self.Tn
