@@ -30,6 +30,23 @@ def step(q, k, v, dout, mask, **kw):
     return (o.detach(), *torch.autograd.grad(o, leaves, dout))
 
 
+# ---- saved tensors that come back with other strides ----------------------------------
+def test_positions_that_only_the_graph_holds_come_back_contiguous():
+    """A slice of grid positions (height and width 250 apart in memory, 200 tokens used), offloaded: save_on_cpu
+    returns it contiguous, and the allocator may give it the block that the slice had."""
+    q = torch.randn(1, 2, 200, 64, device="cuda")
+    h = torch.randn_like(q)
+    inv_freq, axes = axial_frequencies(64, device="cuda")
+    leaf = q.detach().requires_grad_()
+    want = torch.autograd.grad(apply_rotary(leaf, inv_freq=inv_freq, axes=axes,
+                                            positions=grid_positions(5, 5, 10, device="cuda")[:, :200]), leaf, h)[0]
+    for pin in (False, True):
+        leaf = q.detach().requires_grad_()
+        with torch.autograd.graph.save_on_cpu(pin_memory=pin):
+            y = apply_rotary(leaf, inv_freq=inv_freq, axes=axes, positions=grid_positions(5, 5, 10, device="cuda")[:, :200])
+        assert torch.equal(torch.autograd.grad(y, leaf, h)[0], want)
+
+
 def test_two_threads_on_one_stream():
     """The same shape from two host threads, both on the default stream, each with tensors of its own: each gets
     what it gets alone."""

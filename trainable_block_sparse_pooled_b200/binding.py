@@ -200,6 +200,7 @@ def spa2_sparse_attn_bwd(q, k, v, o, o_lo, lse, dout, B, H, N, d, bq, bkv, mask:
 # (a call of a few tokens is mostly the host's time).
 _POINTER = struct.Struct("@P")
 _ROTARY_SPEC = struct.Struct("@Pi3q5iP2if0q")
+_ROTARY_POSITIONS = struct.Struct("@Pi3qi")   # its first fields: the positions and the number of axes
 _ROTARY_TENSOR = "PPi6q"
 _PACK8_TENSOR = "PPPqq"
 ROTARY_TENSORS = (None, struct.Struct("@" + _ROTARY_TENSOR), struct.Struct("@" + 2 * _ROTARY_TENSOR))
@@ -217,11 +218,20 @@ def rotary_spec(positions, position_bytes, position_stride, pairs, inv_freq, rot
 _ROTARY_INV_FREQ = spa2_rotary_spec.inv_freq.offset
 
 
+def rotary_positions(positions, axes: int) -> tuple:
+    """(address, bytes, strides (batch, axis, token)) of a spa2_rotary_spec for positions [N] or [B, N], with
+    several axes [axes, N] or [B, axes, N]."""
+    st, several = positions.stride(), axes > 1
+    return positions.data_ptr(), positions.element_size(), (st[0] if len(st) > 1 + several else 0,
+                                                            st[-2] if several else 0, st[-1])
+
+
 def rotary_spec_points(spec: bytes, inv_freq, positions) -> bool:
-    """Whether a rotary_spec holds the addresses of these tensors."""
-    at = 0 if positions is None else positions.data_ptr()
-    return _POINTER.unpack_from(spec, 0)[0] == at and \
-        _POINTER.unpack_from(spec, _ROTARY_INV_FREQ)[0] == inv_freq.data_ptr()
+    """Whether a rotary_spec is one of these tensors: their addresses, and the strides and type of the positions."""
+    at, size, *strides, axes = _ROTARY_POSITIONS.unpack_from(spec, 0)
+    if _POINTER.unpack_from(spec, _ROTARY_INV_FREQ)[0] != inv_freq.data_ptr():
+        return False
+    return at == 0 if positions is None else (at, size, tuple(strides)) == rotary_positions(positions, axes)
 
 
 def spa2_rotary(tensors, B, N, d, dtype, spec: spa2_rotary_spec, inverse, stream) -> int:

@@ -127,21 +127,15 @@ def _spec(r: Rotary, B: int, N: int, d: int, device) -> tuple:
         if n_axes != 1:
             raise ValueError("more than one axis needs positions")
     else:
-        if pos.dtype == torch.int32:
-            size = 4
-        elif pos.dtype != torch.int64:
+        if pos.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be int32 or int64")
         want = (N,) if n_axes == 1 else (n_axes, N)
-        shape, st = tuple(pos.shape), pos.stride()
-        if shape == want:
-            stride = (0, st[0] if n_axes > 1 else 0, st[-1])
-        elif shape == (B, *want):
-            stride = (st[0], st[1] if n_axes > 1 else 0, st[-1])
-        else:
+        shape = tuple(pos.shape)
+        if shape != want and shape != (B, *want):
             raise ValueError(f"positions have shape {shape}: {want} or {(B, *want)} is wanted")
         if pos.device != device:
             raise ValueError("positions must be on the device of q")
-        at = pos.data_ptr()
+        at, size, stride = b.rotary_positions(pos, n_axes)
     if f.device != device:
         raise ValueError("inv_freq must be on the device of q")
     if f.stride(0) != 1:
