@@ -47,6 +47,62 @@ def test_positions_that_only_the_graph_holds_come_back_contiguous():
         assert torch.equal(torch.autograd.grad(y, leaf, h)[0], want)
 
 
+# ---- forward mode and tracing ---------------------------------------------------------
+@pytest.mark.parametrize("wanted", [False, True])
+def test_forward_mode_derivatives_of_rotary(wanted):
+    """The map is linear: the tangent is turned as its tensor is, bit for bit."""
+    f = rotary_frequencies(32, device="cuda")[0]
+    q, tq, k = (torch.randn(2, 3, 21, 64, device="cuda") for _ in range(3))
+    pos = torch.arange(21, device="cuda") * 3
+    kw = dict(inv_freq=f, positions=pos, layout="half", scale=1.25)
+    want = apply_rotary(tq, **kw)
+    with fwd_ad.dual_level():
+        dual = fwd_ad.make_dual(q.requires_grad_(wanted), tq)
+        y = fwd_ad.unpack_dual(apply_rotary(dual, **kw))
+        assert y.tangent is not None and torch.equal(y.tangent, want)
+        assert torch.equal(y.primal, apply_rotary(q.detach(), **kw))
+        yq, yk = (fwd_ad.unpack_dual(x) for x in apply_rotary(dual, k, **kw))
+        assert torch.equal(yq.tangent, want) and (yk.tangent is None or not yk.tangent.any())
+        yk, yq = (fwd_ad.unpack_dual(x) for x in apply_rotary(k, dual, **kw))
+        assert torch.equal(yq.tangent, want) and (yk.tangent is None or not yk.tangent.any())
+
+
+def test_reverse_over_forward_mode_of_rotary():
+    f = rotary_frequencies(64, device="cuda")[0]
+    q, t, h = (torch.randn(1, 2, 9, 64, device="cuda") for _ in range(3))
+    t.requires_grad_()
+    with fwd_ad.dual_level():
+        tangent = fwd_ad.unpack_dual(apply_rotary(fwd_ad.make_dual(q, t), inv_freq=f)).tangent
+        (got,) = torch.autograd.grad(tangent, t, h)
+    leaf = q.detach().requires_grad_()
+    assert torch.equal(got, torch.autograd.grad(apply_rotary(leaf, inv_freq=f), leaf, h)[0])
+
+
+@pytest.mark.parametrize("checkpoint", [None, "int8"])
+def test_forward_mode_through_the_attention_is_refused(checkpoint):
+    """The attention has no forward-mode derivative: with rotary in front as without it, the call raises."""
+    q, k, v, _ = problem()
+    m = block_mask(q, k, 0.3, 0.6)
+    r = Rotary(rotary_frequencies(64, device="cuda")[0])
+    for i in range(3):
+        for rotary in (None, r):
+            with fwd_ad.dual_level(), pytest.raises((RuntimeError, NotImplementedError)):
+                xs = [q, k, v]
+                xs[i] = fwd_ad.make_dual(xs[i], torch.ones_like(q))
+                sparse_attention(*xs, mask=m, rotary=rotary, checkpoint=checkpoint)
+
+
+def test_traced_rotary_follows_its_inputs():
+    f = rotary_frequencies(64, device="cuda")[0]
+    q, pos = torch.randn(1, 2, 9, 64, device="cuda"), torch.arange(9, device="cuda")
+    traced = torch.jit.trace(lambda x, p: apply_rotary(x, inv_freq=f, positions=p), (q, pos))
+    q2, pos2, h = torch.randn_like(q).requires_grad_(), pos * 7 + 1, torch.randn_like(q)
+    want = apply_rotary(q2, inv_freq=f, positions=pos2)
+    got = traced(q2, pos2)
+    assert torch.equal(got, want)
+    assert torch.equal(torch.autograd.grad(got, q2, h)[0], torch.autograd.grad(want, q2, h)[0])
+
+
 def test_two_threads_on_one_stream():
     """The same shape from two host threads, both on the default stream, each with tensors of its own: each gets
     what it gets alone."""

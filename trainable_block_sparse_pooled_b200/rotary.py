@@ -21,6 +21,7 @@ import math
 from dataclasses import dataclass
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as b
 
@@ -171,37 +172,54 @@ def _turned(spec, inverse: bool, strides, xs):
 
 
 class RotaryFunction(torch.autograd.Function):
-    """(q, k) turned by r; the backward pass is the same map with the angle negated."""
+    """(q, k) turned by Rotary(inv_freq, positions, *how); the backward pass is the same map with the angle
+    negated, the forward-mode derivative the same map of the tangents."""
 
     @staticmethod
-    def forward(ctx, r: Rotary, inverse: bool, strides, *xs):
+    def forward(ctx, how: tuple, inverse: bool, strides, inv_freq, positions, *xs):
         B, _, N, d = xs[0].shape
-        spec, f = _spec(r, B, N, d, xs[0].device)
-        ctx.save_for_backward(r.inv_freq, r.positions)  # so that a change in between is noticed
-        ctx.r, ctx.spec, ctx.inverse = (r.layout, r.axes, r.scale), spec, inverse
-        ctx.strides = [_dense(x) for x in xs]
+        spec, f = _spec(Rotary(inv_freq, positions, *how), B, N, d, xs[0].device)
+        ctx.save_for_backward(inv_freq, positions)  # so that a change in between is noticed
+        ctx.save_for_forward(inv_freq, positions)
+        ctx.how, ctx.spec, ctx.inverse, ctx.out_strides = how, spec, inverse, strides
+        ctx.strides, ctx.shapes = [_dense(x) for x in xs], [x.shape for x in xs]
         ctx.set_materialize_grads(False)
         return tuple(_turned(spec, inverse, strides, xs))
 
     @staticmethod
+    def jvp(ctx, _how, _inverse, _strides, freq_tangent, _positions, *tangents):
+        if freq_tangent is not None:
+            raise RuntimeError("inv_freq takes no derivative: detach it")
+        at = [i for i, t in enumerate(tangents) if t is not None]
+        turned = iter(RotaryFunction.apply(ctx.how, ctx.inverse, [ctx.out_strides[i] for i in at], *ctx.saved_tensors,
+                                           *[tangents[i] for i in at]))
+        return tuple([next(turned) if t is not None else tangents[at[0]].new_zeros(shape)
+                      for t, shape in zip(tangents, ctx.shapes)])
+
+    @staticmethod
     def backward(ctx, *grads):
         wanted = ctx.needs_input_grad
-        at = [i for i, g in enumerate(grads) if g is not None and wanted[3 + i]]
+        at = [i for i, g in enumerate(grads) if g is not None and wanted[5 + i]]
         out = [None] * len(grads)
         if at:
             inv_freq, positions = ctx.saved_tensors
             strides, xs = [ctx.strides[i] for i in at], [grads[i] for i in at]
             if torch.is_grad_enabled():  # the gradient will be differentiated itself
-                turned = RotaryFunction.apply(Rotary(inv_freq, positions, *ctx.r), not ctx.inverse, strides, *xs)
+                turned = RotaryFunction.apply(ctx.how, not ctx.inverse, strides, inv_freq, positions, *xs)
             else:
                 B, _, N, d = xs[0].shape
                 spec, f = ctx.spec, None
                 if not b.rotary_spec_points(spec, inv_freq, positions):  # copies of the saved tensors
-                    spec, f = _spec(Rotary(inv_freq, positions, *ctx.r), B, N, d, xs[0].device)
+                    spec, f = _spec(Rotary(inv_freq, positions, *ctx.how), B, N, d, xs[0].device)
                 turned = _turned(spec, not ctx.inverse, strides, xs)
             for i, g in zip(at, turned):
                 out[i] = g
-        return (None, None, None, *out)
+        return (None, None, None, None, None, *out)
+
+
+def _has_tangent(*xs) -> bool:
+    """Whether one of xs is a dual tensor of forward-mode differentiation."""
+    return any([forward_ad.unpack_dual(x).tangent is not None for x in xs])
 
 
 def _dense(x):
@@ -221,7 +239,8 @@ def _dense(x):
 
 
 def apply_rotary(q, k=None, *, inv_freq, positions=None, layout: str = "interleaved", axes=None, scale: float = 1.0):
-    """q (and k) [B, H, N, d] turned by their positions; differentiable in q and k.
+    """q (and k) [B, H, N, d] turned by their positions; differentiable in q and k, any number of times and in
+    forward mode too.
 
     inv_freq   fp64 [rotary_dim / 2], radians per position; elements from rotary_dim on
                are passed through
@@ -235,7 +254,6 @@ def apply_rotary(q, k=None, *, inv_freq, positions=None, layout: str = "interlea
     q and k are bf16, fp16 or fp32, of one dtype; their head counts may differ. Returns
     contiguous tensors: q' alone, or (q', k').
     """
-    r = Rotary(inv_freq, positions, layout, axes, float(scale))
     dtype, device = q.dtype, q.device
     if dtype not in _DTYPES or k is not None and k.dtype not in _DTYPES:
         raise TypeError("apply_rotary expects bf16, fp16 or fp32 tensors")
@@ -251,10 +269,10 @@ def apply_rotary(q, k=None, *, inv_freq, positions=None, layout: str = "interlea
         (B, _, N, d), other = q.shape, k.shape
         if other[0] != B or other[2] != N or other[3] != d:
             raise ValueError("q and k must agree in batch, length and head width")
-    if wanted and torch.is_grad_enabled():
-        out = RotaryFunction.apply(r, False, (None, None), *xs)
+    if wanted and torch.is_grad_enabled() or torch.jit.is_tracing() or _has_tangent(inv_freq, *xs):
+        out = RotaryFunction.apply((layout, axes, float(scale)), False, (None, None), inv_freq, positions, *xs)
     else:
         B, _, N, d = q.shape
-        spec, f = _spec(r, B, N, d, device)
+        spec, f = _spec(Rotary(inv_freq, positions, layout, axes, float(scale)), B, N, d, device)
         out = tuple(_turned(spec, False, (None, None), xs))
     return out[0] if k is None else out
