@@ -92,6 +92,12 @@ def test_forward_mode_through_the_attention_is_refused(checkpoint):
                 sparse_attention(*xs, mask=m, rotary=rotary, checkpoint=checkpoint)
 
 
+def test_checkpoints_refuse_forward_mode():
+    x = torch.randn(4, 64, device="cuda")
+    with fwd_ad.dual_level(), pytest.raises(RuntimeError):
+        pack8(fwd_ad.make_dual(x, torch.ones_like(x)))
+
+
 def test_traced_rotary_follows_its_inputs():
     f = rotary_frequencies(64, device="cuda")[0]
     q, pos = torch.randn(1, 2, 9, 64, device="cuda"), torch.arange(9, device="cuda")
@@ -101,6 +107,20 @@ def test_traced_rotary_follows_its_inputs():
     got = traced(q2, pos2)
     assert torch.equal(got, want)
     assert torch.equal(torch.autograd.grad(got, q2, h)[0], torch.autograd.grad(want, q2, h)[0])
+
+
+def test_traced_checkpoints_are_refused():
+    """A trace would hold the buffers, not what fills them."""
+    x = torch.randn(4, 64, device="cuda")
+    with pytest.raises(RuntimeError):
+        torch.jit.trace(lambda t: unpack8(*pack8(t))[0], (x,))
+    kept = pack8(x)
+    with pytest.raises(RuntimeError):
+        torch.jit.trace(lambda t: unpack8(*kept)[0] + t, (x,))
+    q, k, v, _ = problem()
+    with pytest.raises(RuntimeError):   # its mask would be that of the traced inputs
+        torch.jit.trace(lambda *xs: sparse_attention(*xs, 0.3, 0.6, checkpoint="int8"),
+                        tuple(t.requires_grad_() for t in (q, k, v)))
 
 
 def test_two_threads_on_one_stream():

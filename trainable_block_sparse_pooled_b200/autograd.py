@@ -41,7 +41,7 @@ from collections import deque
 import torch
 
 from . import binding as b
-from .checkpoint import Packed
+from .checkpoint import Packed, _check_not_traced
 from .rotary import Rotary, apply_rotary
 
 _cache: dict = {}
@@ -280,6 +280,8 @@ def sparse_attention(q, k, v, k_frac: float = 0.0, p_frac: float = 0.0, scale: f
     """
     if checkpoint not in (None, "int8"):
         raise ValueError(f"unknown checkpoint {checkpoint!r}: None or 'int8'")
+    if checkpoint is not None:
+        _check_not_traced("sparse_attention with a checkpoint")
     if rotary is not None:
         q, k = apply_rotary(q, k, inv_freq=rotary.inv_freq, positions=rotary.positions, layout=rotary.layout,
                             axes=rotary.axes, scale=rotary.scale)

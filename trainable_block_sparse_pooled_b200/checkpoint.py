@@ -13,13 +13,15 @@ infinity or a NaN reads back as NaN.
 
 `sparse_attention(..., checkpoint="int8")` keeps its q, k, v this way for the backward
 pass. `pack8` and `unpack8` are for whatever else a training step holds between
-its passes; they are not differentiable (they return detached tensors) and may be
-captured into a CUDA graph.
+its passes; they are not differentiable (they return detached tensors; inputs with a
+forward-mode tangent are refused, and so are traces of torch.jit) and may be captured
+into a CUDA graph.
 """
 
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding as b
 
@@ -100,10 +102,16 @@ def _launch(call, items, dtype, device, what):
             raise b.Spa2Error(rc, what)
 
 
+def _check_not_traced(what):
+    if torch.jit.is_tracing():
+        raise RuntimeError(f"{what} cannot be traced: a trace would hold its buffers and not what fills them")
+
+
 def pack8(*xs: torch.Tensor) -> tuple[Packed, ...]:
     """8-bit checkpoints of CUDA tensors of one dtype (bf16, fp16 or fp32) and any shapes."""
     if not xs:
         raise ValueError("pack8 expects at least one tensor")
+    _check_not_traced("pack8")
     dtype, device = xs[0].dtype, xs[0].device
     if dtype not in _DTYPES:
         raise TypeError(f"pack8 expects bf16, fp16 or fp32 tensors, got {dtype}")
@@ -116,6 +124,8 @@ def pack8(*xs: torch.Tensor) -> tuple[Packed, ...]:
             raise ValueError("pack8 expects tensors on one CUDA device")
         if x.dim() < 1 or x.shape[-1] < 1:
             raise ValueError("pack8 expects tensors of at least one dimension, the last of them not empty")
+        if forward_ad.unpack_dual(x).tangent is not None:
+            raise RuntimeError("pack8 has no forward-mode derivative")
         items.append((Packed.empty_like(x), x if x.is_contiguous() else x.detach().contiguous()))
     _launch(b.lib().spa2_pack8, items, dtype, device, "spa2_pack8")
     return tuple([p for p, _ in items])
@@ -125,6 +135,7 @@ def unpack8(*packed: Packed) -> tuple[torch.Tensor, ...]:
     """The kept values of each checkpoint, contiguous, in its tensor's shape and dtype."""
     if not packed:
         raise ValueError("unpack8 expects at least one checkpoint")
+    _check_not_traced("unpack8")
     dtype, device = packed[0].dtype, packed[0].base.device
     for p in packed:
         if p.dtype != dtype:
