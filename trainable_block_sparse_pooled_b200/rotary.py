@@ -67,7 +67,7 @@ def rotary_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str | N
             return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(theta))
 
         low = max(math.floor(pair_of(beta_fast)), 0)
-        high = min(math.ceil(pair_of(beta_slow)), rotary_dim // 2 - 1)
+        high = min(math.ceil(pair_of(beta_slow)), rotary_dim - 1)  # may lie behind the last pair, rotary_dim / 2 - 1
         ramp = ((p - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)  # 0: kept, 1: divided
         inv_freq = inv_freq * (1.0 - ramp) + inv_freq / factor * ramp
         scale = 0.1 * math.log(factor) + 1.0
