@@ -123,6 +123,48 @@ def test_traced_checkpoints_are_refused():
                         tuple(t.requires_grad_() for t in (q, k, v)))
 
 
+# ---- streams and threads --------------------------------------------------------------
+def test_many_calls_ahead_wait_for_their_own_stream_alone():
+    """Forty calls while another stream is busy for much longer: the calls return, and
+    check_errors too, before that stream is done."""
+    q, k, v, _ = problem(N=256)
+    m = block_mask(q, k, 0.3, 0.6)
+    sparse_attention(q, k, v, mask=m)
+    check_errors()
+    torch.cuda.synchronize()
+    side, busy = torch.cuda.Stream(), torch.cuda.Event()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(6_000_000_000)     # about three seconds
+        busy.record()
+    torch.cuda._sleep(200_000_000)           # a tenth of a second: the status copies are behind it
+    for _ in range(40):
+        sparse_attention(q, k, v, mask=m)
+    assert not busy.query()
+    check_errors()
+    assert not busy.query()
+    torch.cuda.synchronize()
+
+
+def test_errors_are_reported_while_another_stream_is_busy():
+    q, k, v, _ = problem(N=256)
+    m = block_mask(q, k, 1.0, 1.0)
+    check_errors()
+    bad = v.clone()
+    bad[0, 0, 3, 3] = 1e6
+    side, busy = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(6_000_000_000)
+        busy.record()
+    sparse_attention(q, k, bad, mask=m)
+    with pytest.raises(b.Spa2Error) as e:
+        check_errors()
+    assert e.value.code == b.ERR_RANGE and not busy.query()
+    torch.cuda.synchronize()
+    sparse_attention(q, k, v, mask=m)
+    check_errors()
+
+
 def test_two_threads_on_one_stream():
     """The same shape from two host threads, both on the default stream, each with tensors of its own: each gets
     what it gets alone."""

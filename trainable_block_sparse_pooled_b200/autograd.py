@@ -36,6 +36,7 @@ gradients there. `rotary=` turns q and k by their positions first (module `rotar
 from __future__ import annotations
 
 import threading
+import time
 from collections import deque
 
 import torch
@@ -65,7 +66,7 @@ class _StatusWatch:
     def after(self, ops):
         """Queue a copy of the status words of `ops` behind the work just launched."""
         if len(self.pending) == self.SLOTS:
-            self._finish(wait=True)
+            self._finish()
         slot = self.next
         self.next = (self.next + 1) % self.SLOTS
         at, stream = self.host.data_ptr() + 12 * slot, b._stream(torch)
@@ -75,28 +76,42 @@ class _StatusWatch:
         self.pending.append((slot, ops))
 
     def poll(self):
-        """Raise the first error among copies that have landed (never waits)."""
+        """Raise the first error among copies that have landed (never waits for one that has not, but once
+        there is an error, for the others of this stream)."""
         while self.pending and self._landed():
-            self._finish(wait=False)
+            self._finish()
 
     def drain(self):
         """Wait for every pending copy, then raise the first error among them."""
         while self.pending:
-            self._finish(wait=True)
+            self._finish()
 
     def _landed(self):
         slot, ops = self.pending[0]
         return self.codes[slot, len(ops) - 1] != self.PENDING   # the copies of a slot land in order
 
-    def _finish(self, wait):
-        if wait and not self._landed():
-            torch.cuda.synchronize(self.spa.device)
+    def _wait(self):
+        """Until the oldest pending copy has landed: by looking at its word, so that nothing but the work in front
+        of it is waited for, on this stream or another (an event for every call would cost each of them a
+        microsecond). A copy that a failed context will never make ends the wait with that failure."""
+        pause, check_at = 2e-5, time.monotonic() + 0.5
+        while not self._landed():
+            time.sleep(pause)
+            pause = min(2 * pause, 2e-4)
+            if time.monotonic() > check_at:
+                check_at += 0.5
+                if not torch.cuda.is_current_stream_capturing():   # a query would end the capture
+                    torch.cuda.current_stream(self.spa.device).query()
+
+    def _finish(self):
+        self._wait()
         slot, ops = self.pending.popleft()
         for col, op in enumerate(ops):
             code = int(self.codes[slot, col])
             if code != b.OK:
-                torch.cuda.synchronize(self.spa.device)  # no copy lands in a slot that is used again
-                self.pending.clear()
+                while self.pending:   # this stream's other calls: only the first error is raised
+                    self._wait()
+                    self.pending.popleft()
                 raise b.Spa2Error(code, f"device status of sparse_attention (op {op})")
 
 
