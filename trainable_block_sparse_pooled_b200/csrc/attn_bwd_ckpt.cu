@@ -104,7 +104,6 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   const uint32_t lane = lane_id();
   const int i = blockIdx.x;
   const int bh = blockIdx.y;
-  pdl_trigger();
   const long long rowid = (long long)bh * Tm + i;
 
   // what the start waits for, asked for at once: the row's count and first block, and (warps
@@ -158,6 +157,10 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  // Not before this block has its tensor memory: a dK/dV block takes all of an SM's and waits for this grid's
+  // end, so it must not come between this block's start and its allocation (by registers the two do not fit
+  // on one SM today, by shared memory at d = 64 they would).
+  pdl_trigger();
   const WaitCtx wc{&sm.abort_flag, status, wait_limit_ns};
   const WaitCtx drain_wc{&sm.never, nullptr, wait_limit_ns};
 
