@@ -124,7 +124,7 @@ def pack8(*xs: torch.Tensor) -> tuple[Packed, ...]:
             raise ValueError("pack8 expects tensors on one CUDA device")
         if x.dim() < 1 or x.shape[-1] < 1:
             raise ValueError("pack8 expects tensors of at least one dimension, the last of them not empty")
-        if forward_ad.unpack_dual(x).tangent is not None:
+        if forward_ad._current_level >= 0 and forward_ad.unpack_dual(x).tangent is not None:
             raise RuntimeError("pack8 has no forward-mode derivative")
         items.append((Packed.empty_like(x), x if x.is_contiguous() else x.detach().contiguous()))
     _launch(b.lib().spa2_pack8, items, dtype, device, "spa2_pack8")

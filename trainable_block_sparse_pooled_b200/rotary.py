@@ -180,9 +180,11 @@ class RotaryFunction(torch.autograd.Function):
         B, _, N, d = xs[0].shape
         spec, f = _spec(Rotary(inv_freq, positions, *how), B, N, d, xs[0].device)
         ctx.save_for_backward(inv_freq, positions)  # so that a change in between is noticed
-        ctx.save_for_forward(inv_freq, positions)
-        ctx.how, ctx.spec, ctx.inverse, ctx.out_strides = how, spec, inverse, strides
-        ctx.strides, ctx.shapes = [_dense(x) for x in xs], [x.shape for x in xs]
+        ctx.how, ctx.spec, ctx.inverse = how, spec, inverse
+        ctx.strides = [_dense(x) for x in xs]
+        if forward_ad._current_level >= 0:  # for jvp, which follows at once
+            ctx.save_for_forward(inv_freq, positions)
+            ctx.out_strides, ctx.shapes = strides, [x.shape for x in xs]
         ctx.set_materialize_grads(False)
         return tuple(_turned(spec, inverse, strides, xs))
 
@@ -219,7 +221,7 @@ class RotaryFunction(torch.autograd.Function):
 
 def _has_tangent(*xs) -> bool:
     """Whether one of xs is a dual tensor of forward-mode differentiation."""
-    return any([forward_ad.unpack_dual(x).tangent is not None for x in xs])
+    return forward_ad._current_level >= 0 and any([forward_ad.unpack_dual(x).tangent is not None for x in xs])
 
 
 def _dense(x):
