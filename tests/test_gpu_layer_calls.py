@@ -192,3 +192,39 @@ def test_two_threads_on_one_stream():
         t.join()
     check_errors()
     assert right == [60, 60]
+
+
+# ---- masks that are filled again ------------------------------------------------------
+@pytest.mark.parametrize("how", ["block_mask", "in place"])
+def test_a_mask_changed_before_the_backward_pass_is_noticed(how):
+    """The gradients are those of the attention under the mask's lists as they are in the backward pass: not of the
+    o that was returned, if they are others by then."""
+    q, k, v, dout = problem()
+    s = b.Spa2(1, 2, 500, 64)
+    m = s.block_mask(q, k, 0.2, 0.4)
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    o = sparse_attention(*leaves, mask=m, checkpoint="int8")
+    if how == "block_mask":
+        s.block_mask(k, q, 0.5, 0.9, mask=m)
+    else:
+        m.col_cnt.fill_(1)
+    with pytest.raises(RuntimeError, match="mask"):
+        torch.autograd.grad(o, leaves, dout)
+
+
+def test_other_lists_put_into_a_mask_do_not_reach_the_backward_pass():
+    q, k, v, dout = problem()
+    m, other = block_mask(q, k, 0.2, 0.4), block_mask(q, k, 0.6, 0.9)
+    want = step(q, k, v, dout, b.Mask(m.row_cnt, m.row_idx, m.col_cnt, m.col_idx))
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    o = sparse_attention(*leaves, mask=m, checkpoint="int8")
+    m.row_cnt, m.row_idx, m.col_cnt, m.col_idx = other.row_cnt, other.row_idx, other.col_cnt, other.col_idx
+    assert all(torch.equal(a, w) for a, w in zip(torch.autograd.grad(o, leaves, dout), want[1:]))
+
+
+def test_a_mask_built_in_inference_mode_serves_a_training_step():
+    q, k, v, dout = problem()
+    with torch.inference_mode():
+        frozen = block_mask(q, k, 0.2, 0.6)
+    want = step(q, k, v, dout, block_mask(q, k, 0.2, 0.6))
+    assert all(torch.equal(a, w) for a, w in zip(step(q, k, v, dout, frozen), want))

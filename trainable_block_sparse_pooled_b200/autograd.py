@@ -218,7 +218,8 @@ class CheckpointedAttentionFunction(torch.autograd.Function):
             o, kept = s.fwd_ckpt(q, k, v, mask, scale)
             s.watch.after((b.OP_FWD,))
         ctx.save_for_backward(kept[0].base)
-        ctx.mask, ctx.scale, ctx.spa = mask, scale, s
+        ctx.mask, ctx.scale, ctx.spa = mask.lists(), scale, s
+        ctx.versions = ctx.mask.versions()
         return o
 
     @staticmethod
@@ -230,6 +231,9 @@ class CheckpointedAttentionFunction(torch.autograd.Function):
 
 def _checkpointed_backward(ctx, do):
     s = ctx.spa
+    if ctx.mask.versions() != ctx.versions:
+        raise RuntimeError("the lists of the block mask were changed in place after sparse_attention: the backward pass "
+                           "would be that of another attention than the one whose o it returned")
     if torch.cuda.is_current_stream_capturing():
         s = _spa(s.B, s.H, s.N, s.d, s.device, s.bq, s.bkv)
     kept, do = Packed.several_in(ctx.saved_tensors[0], do.shape, do.dtype, 3), do.contiguous()

@@ -315,6 +315,15 @@ class Mask:
         return spa2_mask(p(self.row_cnt), p(self.row_idx), p(self.col_cnt), p(self.col_idx), p(self.pbar),
                          p(self.bitmap))
 
+    def lists(self) -> "Mask":
+        """The four lists, in a Mask of their own."""
+        return Mask(self.row_cnt, self.row_idx, self.col_cnt, self.col_idx)
+
+    def versions(self) -> tuple:
+        """A number for each list that changes when it is written in place (0 where torch does not count)."""
+        return tuple([0 if t is None or t.is_inference() else t._version
+                      for t in (self.row_cnt, self.row_idx, self.col_cnt, self.col_idx)])
+
     def kept_blocks(self) -> int:
         return int(self.row_cnt.sum().item())
 
@@ -397,7 +406,11 @@ class Spa2:
                     t.empty(B, H, Tm, Tn, dtype=t.uint8, device=self.device) if self.with_bitmap else None)
 
     def block_mask(self, q, k, k_frac, p_frac, mask: Mask | None = None) -> Mask:
-        mask = mask or self.new_mask()
+        if mask is None:
+            mask = self.new_mask()
+        else:   # torch does not see what the kernels write
+            self.torch.autograd.graph.increment_version(
+                [t for t in vars(mask).values() if t is not None and not t.is_inference()])
         cm = mask.c()
         ws = self.ws[OP_MASK]
         _check(spa2_block_mask(q.data_ptr(), k.data_ptr(), self.B, self.H, self.N, self.d, self.bq, self.bkv,
