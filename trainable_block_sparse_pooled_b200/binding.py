@@ -452,10 +452,17 @@ class Spa2:
                                     _stream(t)), "spa2_sparse_attn_bwd")
         return dq, dk, dv
 
+    def _expect(self, name, x):
+        want = (self.B, self.H, self.N, self.d)
+        if x.shape != want or x.dtype != self.torch.bfloat16 or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous bf16 {want}")
+
     def fwd_ckpt(self, q, k, v, mask: Mask, scale=0.0, lse=None):
         """O (bf16) and the 8-bit checkpoints of q, k, v (checkpoint.Packed), all that bwd_ckpt needs."""
         from .checkpoint import Packed
         t = self.torch
+        for name, x in (("q", q), ("k", k), ("v", v)):
+            self._expect(name, x)
         o = t.empty_like(q)
         kept = Packed.several_like(q, 3)
         cm = mask.c()
@@ -469,6 +476,9 @@ class Spa2:
     def bwd_ckpt(self, kept, dout, mask: Mask, scale=0.0, grad_dtype=DTYPE_F32):
         """dQ, dK, dV at the values of the checkpoints `kept` (from fwd_ckpt or checkpoint.pack8)."""
         t = self.torch
+        self._expect("dout", dout)
+        if len(kept) != 3 or any([p.shape != dout.shape for p in kept]):
+            raise ValueError("bwd_ckpt expects the checkpoints of q, k and v, of dout's shape")
         gt = t.float32 if grad_dtype == DTYPE_F32 else t.bfloat16
         dq, dk, dv = (t.empty_like(dout, dtype=gt) for _ in range(3))
         cm = mask.c()
