@@ -228,3 +228,23 @@ def test_a_mask_built_in_inference_mode_serves_a_training_step():
         frozen = block_mask(q, k, 0.2, 0.6)
     want = step(q, k, v, dout, block_mask(q, k, 0.2, 0.6))
     assert all(torch.equal(a, w) for a, w in zip(step(q, k, v, dout, frozen), want))
+
+
+# ---- C entry points -------------------------------------------------------------------
+def test_rotary_through_the_binding():
+    """spa2_rotary with its structures: rows of a wider buffer turned into another, nothing beside them written."""
+    f = rotary_frequencies(32, device="cuda")[0]
+    x = torch.randn(2, 3, 21, 40, device="cuda").to(BF16)
+    y = torch.full((2, 3, 21, 40), 55.0, device="cuda").to(BF16)
+    t = b.spa2_rotary_tensor(x.data_ptr(), y.data_ptr(), 3)
+    t.x_stride[:] = t.y_stride[:] = x.stride()[:3]
+    s = b.spa2_rotary_spec()
+    s.axes, s.inv_freq, s.rotary_dim, s.layout, s.scale = 1, f.data_ptr(), 32, b.ROTARY_HALF, 1.5
+    s.pairs[0] = 16
+    stream = torch.cuda.current_stream().cuda_stream
+    for inverse in (False, True):
+        assert b.spa2_rotary((b.spa2_rotary_tensor * 1)(t), 2, 21, 36, b.DTYPE_BF16, s, inverse, stream) == b.OK
+        leaf = x[..., :36].detach().requires_grad_()
+        out = apply_rotary(leaf, inv_freq=f, layout="half", scale=1.5)
+        want = torch.autograd.grad(out, leaf, leaf.detach())[0] if inverse else out.detach()
+        assert torch.equal(y[..., :36], want) and (y[..., 36:] == 55.0).all()
