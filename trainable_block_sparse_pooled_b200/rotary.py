@@ -256,6 +256,8 @@ def apply_rotary(q, k=None, *, inv_freq, positions=None, layout: str = "interlea
     q and k are bf16, fp16 or fp32, of one dtype; their head counts may differ. Returns
     contiguous tensors: q' alone, or (q', k').
     """
+    if getattr(scale, "requires_grad", False):
+        raise ValueError("scale takes no gradient: give a number")
     dtype, device = q.dtype, q.device
     if dtype not in _DTYPES or k is not None and k.dtype not in _DTYPES:
         raise TypeError("apply_rotary expects bf16, fp16 or fp32 tensors")
