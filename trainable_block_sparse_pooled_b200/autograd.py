@@ -104,7 +104,8 @@ class _StatusWatch:
                     torch.cuda.current_stream(self.spa.device).query()
 
     def _finish(self):
-        self._wait()
+        if not self._landed():
+            self._wait()
         slot, ops = self.pending.popleft()
         for col, op in enumerate(ops):
             code = int(self.codes[slot, col])

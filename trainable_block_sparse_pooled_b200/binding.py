@@ -320,9 +320,12 @@ class Mask:
         return Mask(self.row_cnt, self.row_idx, self.col_cnt, self.col_idx)
 
     def versions(self) -> tuple:
-        """A number for each list that changes when it is written in place (0 where torch does not count)."""
-        return tuple([0 if t is None or t.is_inference() else t._version
-                      for t in (self.row_cnt, self.row_idx, self.col_cnt, self.col_idx)])
+        """A number for each list that changes when it is written in place; () where torch does not count (lists
+        made in inference mode)."""
+        try:
+            return self.row_cnt._version, self.row_idx._version, self.col_cnt._version, self.col_idx._version
+        except RuntimeError:
+            return ()
 
     def kept_blocks(self) -> int:
         return int(self.row_cnt.sum().item())
@@ -452,17 +455,17 @@ class Spa2:
                                     _stream(t)), "spa2_sparse_attn_bwd")
         return dq, dk, dv
 
-    def _expect(self, name, x):
-        want = (self.B, self.H, self.N, self.d)
-        if x.shape != want or x.dtype != self.torch.bfloat16 or not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous bf16 {want}")
+    def _expect(self, names, *xs):
+        want, bf16 = (self.B, self.H, self.N, self.d), self.torch.bfloat16
+        for x in xs:
+            if x.shape != want or x.dtype != bf16 or not x.is_contiguous():
+                raise ValueError(f"{names} must be contiguous bf16 {want}")
 
     def fwd_ckpt(self, q, k, v, mask: Mask, scale=0.0, lse=None):
         """O (bf16) and the 8-bit checkpoints of q, k, v (checkpoint.Packed), all that bwd_ckpt needs."""
         from .checkpoint import Packed
         t = self.torch
-        for name, x in (("q", q), ("k", k), ("v", v)):
-            self._expect(name, x)
+        self._expect("q, k, v", q, k, v)
         o = t.empty_like(q)
         kept = Packed.several_like(q, 3)
         cm = mask.c()
@@ -477,13 +480,14 @@ class Spa2:
         """dQ, dK, dV at the values of the checkpoints `kept` (from fwd_ckpt or checkpoint.pack8)."""
         t = self.torch
         self._expect("dout", dout)
-        if len(kept) != 3 or any([p.shape != dout.shape for p in kept]):
+        q8, k8, v8 = kept
+        if not q8.shape == k8.shape == v8.shape == dout.shape:
             raise ValueError("bwd_ckpt expects the checkpoints of q, k and v, of dout's shape")
         gt = t.float32 if grad_dtype == DTYPE_F32 else t.bfloat16
         dq, dk, dv = (t.empty_like(dout, dtype=gt) for _ in range(3))
         cm = mask.c()
         ws = self.ws[OP_BWD_CKPT]
-        _check(spa2_sparse_attn_bwd_ckpt(*(p.c() for p in kept), dout.data_ptr(), self.B, self.H, self.N, self.d,
+        _check(spa2_sparse_attn_bwd_ckpt(q8.c(), k8.c(), v8.c(), dout.data_ptr(), self.B, self.H, self.N, self.d,
                                          self.bq, self.bkv, cm, float(scale), dq.data_ptr(), dk.data_ptr(),
                                          dv.data_ptr(), int(grad_dtype), ws.data_ptr(), ws.numel(), _stream(t)),
                "spa2_sparse_attn_bwd_ckpt")
