@@ -250,8 +250,8 @@ SPA2_API spa2_status spa2_sparse_attn_bwd(const void* q, const void* k, const vo
  *   (a, b) -> scale * (a cos theta - b sin theta, a sin theta + b cos theta),
  * and elements rd .. d - 1 are copied as they are. `inverse` turns by -theta,
  * the transpose of the forward map, which is its backward pass.
- * Angles are reduced in fp64 (good to fp32 accuracy while |theta| < 2^31), the
- * rotation runs in fp32 and is rounded once to the element type.
+ * Angles are formed and reduced in fp64 (off by at most 3.4e-16 |theta| rad: below fp32's 2^-24
+ * while |theta| < 2^27), the rotation runs in fp32 and is rounded once to the element type.
  *   t, n      : 1 or 2 tensors (queries and keys) of the same B, N, d and type
  *               turned by one launch; heads may differ. Strides are in elements
  *               (batch, head, token); the d elements of a row are contiguous.
@@ -326,8 +326,8 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
 /*
  * The sparse attention step on 8-bit checkpoints. spa2_sparse_attn_fwd_ckpt is
  * spa2_sparse_attn_fwd (same o, bit for bit) and also writes q, k, v as 8-bit
- * checkpoints; nothing else needs to be kept for the backward pass (3.1 bytes per
- * element of q instead of the 10 of q, k, v, o and o_lo in bf16).
+ * checkpoints; beside the mask's lists nothing else needs to be kept for the backward
+ * pass (3.1 bytes per element of q instead of the 10 of q, k, v, o and o_lo in bf16).
  * spa2_sparse_attn_bwd_ckpt reads the checkpoints, finds the LSE of their values
  * and D = rowsum(dO * O) = sum_j P_ij dP_ij again (O itself is not computed) and
  * writes dQ, dK, dV: the gradients of the attention at the kept values. Products

@@ -28,9 +28,9 @@ pass wants leaves that no live eager graph holds (torch ends the capture with an
 exception otherwise).
 
 `sparse_attention(..., checkpoint="int8")` keeps q, k and v for the backward pass as
-8-bit checkpoints (module `checkpoint`) and nothing else of their size; the
-backward pass computes the attention again from the kept values and returns its
-gradients there. `rotary=` turns q and k by their positions first (module `rotary`).
+8-bit checkpoints (module `checkpoint`) and the mask's lists, nothing else of their
+size; the backward pass computes the attention again from the kept values and
+returns its gradients there. `rotary=` turns q and k by their positions first (module `rotary`).
 """
 
 from __future__ import annotations
@@ -294,6 +294,7 @@ def sparse_attention(q, k, v, k_frac: float = 0.0, p_frac: float = 0.0, scale: f
     checkpoint="int8" keeps q, k, v in 8 bits for the backward pass (3.1 bytes per
     element of q in place of 10) and computes the attention again there: the same o,
     and its gradients at the kept values. Where no gradient is wanted nothing is kept.
+    The mask's lists must not change before the backward pass, which raises if they did.
 
     `rotary` turns q and k before the mask and the attention; the mask given by
     `mask` is one of turned q and k.

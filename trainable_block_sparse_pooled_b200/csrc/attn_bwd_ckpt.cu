@@ -29,9 +29,9 @@
 // this one's start and end. That fixes the layout: 256 columns of tensor memory and 113 KB
 // of shared memory each, hence Q and dO in shared memory (SS products, bound by the 128
 // bytes a cycle that the tensor core reads there), K double-buffered and V single. At
-// [12, 32760, 128] with 25.6 of 512 blocks kept: 830 us; the products' shared-memory and tensor
-// cycles alone (768 a tile in the first pass, 1024 in the second, 531 tiles an SM) would take 560 us
-// at the 1.7 GHz that the power limit leaves. Measured and not kept: one CTA an SM with Q and dO in
+// [12, 32760, 128] with 25.6 of 512 blocks kept: 900 us; the products' shared-memory and tensor
+// cycles alone (768 a tile in the first pass, 1280 in the second, 531 tiles an SM) would take 640 us
+// at the 1.7 GHz that the power limit leaves. Measured and not kept (with dS as one half): one CTA an SM with Q and dO in
 // tensor memory (as bwd_dq_kernel) 1000 us, that with 16 warps 1064; here, Q and dO in tensor memory
 // for the first pass 945 against 906, three buffers filled in turn by K and V 914 against 906.
 // The forward again for LSE and O (both halves of O stored and read, an fp16 V) took 333 + 34 + 50

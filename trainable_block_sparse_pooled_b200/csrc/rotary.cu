@@ -88,7 +88,7 @@ SPA2_DEV void turn(float x, float y, float2 cs, float& ox, float& oy) {
 // SPLIT: a unit is V elements and their V partners elsewhere in the row (the half layout; single
 // elements of the interleaved one).
 // Registers against loads in flight, measured: the interleaved units do best with four heads' loads
-// together and 78 registers (three blocks an SM): 490 us at the 14B shape above; with no block count
+// together and 75 registers (three blocks an SM): 490 us at the 14B shape above; with no block count
 // asked for the compiler took 66 registers and 580 us, with four blocks (64) 524, two heads at a time
 // 501 to 519, eight 493 to 684. SPLIT units hold twice the angles: one head (two loads) at a time and
 // four blocks an SM (64 registers) take 80 us for [1, 12, 32760, 128] twice, two heads and two blocks
@@ -115,8 +115,10 @@ __global__ void __launch_bounds__(256, SPLIT ? (V == 8 ? 4 : 5) : 1) rotary_kern
       for (int i = 0; i < PAIRS; ++i) cs[i] = cos_sin(a, b, n, u * PAIRS + i);
     }
   } else {
-    // part of the head: the warp shares the angles of its few turning threads out evenly (an
-    // eighth of 64 elements turned, 4 heads: 67 us a launch, 82 with every thread on its own)
+    // part of the head: the warp shares the angles of its few turning threads out evenly. It counts where
+    // a token has few heads (an eighth of 64 elements turned, 4 heads: 67 us a launch, 82 with every thread on
+    // its own); q and k [1, 12, 32760, 128], an eighth or a quarter turned: 72 and 73 us against 73 and 75
+    // interleaved, 103 and 102 against 109 and 106 in the half layout, for 61 us of bytes
     __shared__ float2 angle[8][32 * PAIRS];
     __shared__ int3 unit[8][32];
     const int w = threadIdx.x >> 5;
