@@ -7,7 +7,8 @@ import torch.utils.checkpoint
 
 from trainable_block_sparse_pooled_b200 import synth
 from trainable_block_sparse_pooled_b200.autograd import check_errors, sparse_attention
-from trainable_block_sparse_pooled_b200.rotary import Rotary, axial_frequencies, grid_positions
+from trainable_block_sparse_pooled_b200.checkpoint import pack8, unpack8
+from trainable_block_sparse_pooled_b200.rotary import Rotary, apply_rotary, axial_frequencies, grid_positions, rotary_frequencies
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +111,24 @@ def test_one_tensor_for_all_three(layer):
     # three bf16 gradients added up in bf16, in the order of their arrival: half a step of each sum, 2^-8 of it
     total = sum(w.double() for w in want)
     assert ((got.double() - total).abs() <= 2 * 2.0 ** -8 * (sum(w.double().abs() for w in want))).all()
+
+
+def test_function_transforms_are_refused(layer):
+    """torch.func has no rule for these calls, and hands them tensors without memory: they raise, and do not run past
+    the transform."""
+    run, q, k, v, _ = layer
+    f = rotary_frequencies(64, device="cuda")[0]
+    x = torch.randn(2, 1, 2, 8, 64, device="cuda")
+    for call in (lambda t: apply_rotary(t, inv_freq=f), lambda t: unpack8(*pack8(t))[0]):
+        with pytest.raises(RuntimeError):
+            torch.func.jvp(call, (x[0],), (torch.ones_like(x[0]),))
+        with pytest.raises(RuntimeError):
+            torch.func.grad(lambda t: call(t).sum())(x[0])
+        with pytest.raises(RuntimeError):
+            torch.func.vmap(call)(x)
+        with pytest.raises(RuntimeError):
+            torch.func.vmap(call, in_dims=4)(x.movedim(0, 4))
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(run, (q, k, v), (torch.ones_like(q),) * 3)
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda t: run(t, k, v).float().sum())(q)
