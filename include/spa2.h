@@ -334,12 +334,14 @@ SPA2_API spa2_status spa2_unpack8(const spa2_pack8_tensor* t, int n, int dtype, 
  * take fp16 operands and add up in fp32: the kept values (exact where a group's
  * largest magnitude is between 4e-6 and 65504; beyond, clamped and reported as
  * SPA2_ERR_RANGE), P and dS (11 bits each; in dQ = dS K dS is a pair of halves, 22 bits), and dO times a power of two
- * that brings the largest |dO| into [4, 8), lower where |V| is above 16 (so that dS
- * stays in range): the row's largest for dQ, so that every row of dQ has its full precision;
- * the head's largest for dK and dV, whose precision is relative to it (an element of dO,
- * or a dS, below 2^-17 of it loses bits, below 2^-27 everything). dO may have any size that
- * bf16 holds; infinities, NaN and what |V| above 16 takes past its range are reported as
- * SPA2_ERR_RANGE.
+ * that brings the largest |dS| that it and V allow to 2^15 (dO to 2^15 at most): with the
+ * row's largest |dO| for dQ, so that every row of dQ has its full precision; with the
+ * head's largest for dK and dV, whose precision is relative to it (with |V| up to 8 an
+ * element of dO below 2^-20 of it loses bits, a dS below 2^-17, and both everything
+ * below 2^-28). dO may have any size that bf16 holds; infinities, NaN and what |V| above
+ * 16 takes past its range are reported as SPA2_ERR_RANGE. Kept values below 4e-6 are off
+ * by up to 2^-25, not reported: with V, or K and Q, that small altogether their gradients are
+ * as inexact as those.
  * Keeping O and LSE instead of recomputing them is cheaper but not close: with q,
  * k, v rounded to 8 bits and O, LSE not, the rows of dS no longer sum to zero,
  * and sink keys of 8x norm amplify that to 12% of dQ (4% with recomputation).

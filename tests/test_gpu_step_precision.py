@@ -117,3 +117,22 @@ def test_gradients_of_any_size_that_bf16_holds(power):
     s.check()
     for g, w in zip(got, want):
         assert ((g.double() - torch.ldexp(w.double(), by)).abs() <= 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("power", [4, 8, 10])
+def test_small_values(d, power):
+    """V at 2^-power: dQ and dK are 2^-power of what they were, dV is the same, bit for bit. dP is exact in dO's and
+    V's powers of two, and dO is taken up by as much as V has gone down (2^12 in all, of which |V| of 4 to 8
+    takes 1 or 2), so dS is rounded as before. dO in whole numbers, which fp16 holds however they are scaled."""
+    q, k, v, dout = normal(2000, d, seed=power)
+    dout = (2 * dout.float()).round().to(BF16)
+    assert 4 <= v.abs().max() < 8
+    s = b.Spa2(1, 1, 2000, d)
+    m = s.block_mask(q, k, 1.0, 1.0)
+    want = s.bwd_ckpt(pack8(q, k, v), dout, m)
+    by = torch.tensor(-power, device="cuda")
+    got = s.bwd_ckpt(pack8(q, k, torch.ldexp(v.float(), by).to(BF16)), dout, m)
+    s.check()
+    assert torch.equal(got[0], torch.ldexp(want[0], by)) and torch.equal(got[1], torch.ldexp(want[1], by))
+    assert torch.equal(got[2], want[2])

@@ -15,9 +15,9 @@
 // Precision: every product takes fp16 operands and adds up in fp32, in this pass as in the dK/dV
 // pass. The kept values have 7 bits and are exact in fp16 (a group whose largest magnitude is
 // below 4e-6 loses up to 2^-25; above 65504 is clamped and reported). dO is multiplied by a power
-// of two that brings the largest |dO| into [4, 8) (lower where V is above 16: dS must not leave fp16's
-// range; gradients are linear in dO, and the loss's scale must not decide what is left of them), which
-// leaves its 8 bits exact down to 2^-19 of the largest. Here that is the row's largest, since a row of dQ depends on
+// of two that brings the largest |dO| into [4, 8), and on until the largest |dS| that V allows is 2^15 (gradients
+// are linear in dO and V: neither the loss's scale nor V's must decide what fp16 leaves of them). With V
+// between 4 and 8 that leaves dO's 8 bits exact down to 2^-20 of the largest. Here that is the row's largest, since a row of dQ depends on
 // no other row of dO; in the dK/dV pass, whose sums run over the rows, it is the head's. With the head's
 // factor alone a row of 2^-12 of the largest would lose 4e-3 of its dQ, one of 2^-16 9e-2. dS, formed in fp32, enters
 // dQ = dS K as a pair of halves, 22 bits (bwd_dq_kernel: a pair of bf16). A single half is off by 7e-4 of
@@ -332,18 +332,18 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
     }
     fence_proxy_async_smem();
     mbar_arrive(&sm.q_ready);
-    // The power of two that brings the largest |dO|, of a row for this pass and of the head for the dK/dV
-    // pass, 2^(E - 127) or more, into [4, 8): its exponent field is 127 + 129 - E (for infinities and NaN,
-    // which are reported, and zeros any will do). With |V| < 2^(F - 126), F its largest exponent, |dP - D| <
-    // d 2^(F - 122) then, and where that could pass 2^15 dO is scaled down further, so that dS stays within
-    // fp16's range.
+    // The power of two that dO is multiplied by. Its exponent field 127 + 129 - E would bring the largest |dO|,
+    // 2^(E - 127) or more (of a row for this pass, of the head for the dK/dV pass), into [4, 8); for infinities
+    // and NaN, which are reported, and zeros any will do. With |V| < 2^(F - 126), F its largest exponent,
+    // |dP - D| < d 2^(F - 122) then: from there it goes down or up until that bound is 2^15, so that dS uses fp16's
+    // range and does not leave it whatever the size of V; up by 2^12 at most, where dO itself reaches 2^15.
     const int v_e = (int)__reduce_max_sync(0xffffffffu, most & 0xffffu);
-    const uint32_t down = (uint32_t)max(0, v_e - 137 + (D == 128 ? 7 : 6));
-    auto factor_e = [&](uint32_t e) { return min(max(e, 3u) + down, 255u); };
+    const int down = max(-12, v_e - 137 + (D == 128 ? 7 : 6));
+    auto factor_e = [&](uint32_t e) { return (uint32_t)min(max((int)max(e, 3u) + down, 3), 255); };
     const uint32_t do_e = __reduce_max_sync(0xffffffffu, most) >> 23, most_e = factor_e(do_e);
     const float do_scale = __uint_as_float((256u - most_e) << 23);
     if (i == 0 && threadIdx.x == 0) unscale[bh] = __uint_as_float((most_e - 2u) << 23);  // its inverse
-    bad = bad || do_e + down > 255u;
+    bad = bad || (int)do_e + down > 255;
     // dO_i to fp16, by its row's factor, and a copy by the head's
 #pragma unroll
     for (int x = 0; x < DO_PIECES; ++x) {
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(DQC_THREADS, 2)
       if (c == 0) sm.row_e[pr] = (uint8_t)row_e;
       auto to16 = [&](uint32_t w, float by) {
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-        return do_e <= 254u ? pack_f16(f.x * by, f.y * by)  // below 8
+        return do_e <= 254u ? pack_f16(f.x * by, f.y * by)  // below 2^15
                             : pack_f16_clamped(f.x * by, f.y * by, bad);
       };
       auto all16 = [&](float by) { return make_uint4(to16(in.x, by), to16(in.y, by), to16(in.z, by), to16(in.w, by)); };
