@@ -19,18 +19,18 @@ pinned host memory; the next call on that shape and stream raises `Spa2Error`
 once such a copy has landed with an error in it, and `check_errors()` waits for
 every pending copy and raises.
 
-Workspaces are cached per (shape, device, CUDA stream) and allocated when an
-operation first needs one: calls on different streams never share scratch memory. Host
-threads that share a stream share its workspaces; a lock keeps the launches of one
-operation together. A call that is captured into a CUDA graph gets workspaces of its own, from the graph's memory, and its device-side errors are not
-reported (a replay reads no status word). As for any torch operator, a captured backward
-pass wants leaves that no live eager graph holds (torch ends the capture with an
-exception otherwise).
+Workspaces are cached per (shape, device, CUDA stream) and allocated when an operation
+first needs one: calls on different streams never share scratch memory. Host threads
+that share a stream share its workspaces; a lock keeps the launches of one operation
+together. A call that is captured into a CUDA graph gets workspaces of its own, from the
+graph's memory, and its device-side errors are not reported (a replay reads no status
+word). As for any torch operator, a captured backward pass wants leaves that no live
+eager graph holds (torch ends the capture with an exception otherwise).
 
 `sparse_attention(..., checkpoint="int8")` keeps q, k and v for the backward pass as
 8-bit checkpoints (module `checkpoint`) and the mask's lists, nothing else of their
-size; the backward pass computes the attention again from the kept values and
-returns its gradients there. `rotary=` turns q and k by their positions first (module `rotary`).
+size; the backward pass computes the attention again from the kept values and returns
+its gradients there. `rotary=` turns q and k by their positions first (module `rotary`).
 """
 
 from __future__ import annotations
